@@ -7,6 +7,7 @@ library is missing the import fails loudly -- there is no fallback path.
 """
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -21,6 +22,9 @@ FMT = {"TERN160": 1, "Q2_0": 2, "Q3": 3, "MXFP4": 4, "Q8": 5}
 FMT_NAME = {v: k for k, v in FMT.items()}
 MAX_DECODE_ROWS = 8
 MAX_TOP_K = 8
+MAX_GROUPS = 1024
+MAX_Q4_ROWS = 64
+T_F32, T_BF16, T_F16 = 0, 1, 2
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_status_string", "moe_packed_bytes", "moe_pack", "moe_unpack",
@@ -28,7 +32,10 @@ EXPORTS = ("moe_status_string", "moe_packed_bytes", "moe_pack", "moe_unpack",
            "moe_layer", "moe_layer_profiled", "moe_stack_decode", "moe_quant_mxfp8",
            "moe_stream_read", "moe_set_spin_limit", "moe_workspace_status", "moe_layer_noalloc",
            "moe_allocate_formats", "moe_cache_create", "moe_cache_destroy", "moe_cache_plan",
-           "moe_copy_share", "moe_cpu_expert_ffn", "moe_add_chain")
+           "moe_copy_share", "moe_cpu_expert_ffn", "moe_add_chain",
+           "moe_group_plan_bytes", "moe_group_plan", "moe_group_matmul", "moe_group_swiglu",
+           "moe_group_matmul_t", "moe_group_swiglu_grad", "moe_group_wgrad", "moe_group_combine",
+           "moe_group_combine_grad", "moe_q4_bytes", "moe_q4_pack", "moe_q4_unpack", "moe_q4_matvec")
 
 
 class MoeError(RuntimeError):
@@ -52,6 +59,27 @@ class LayerWeights(ctypes.Structure):
 class ExpertRef(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
                 ("gate", ctypes.c_uint64), ("up", ctypes.c_uint64), ("down", ctypes.c_uint64)]
+
+
+class GroupDims(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("rows", ctypes.c_int32), ("x_rows", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("src_div", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("ldx", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("ldw", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+                ("ld_pre", ctypes.c_int64)]
+
+
+class CombineDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("top_k", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("o_rows", ctypes.c_int32), ("type", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("ldo", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class Q4Dims(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("n_mats", ctypes.c_int32), ("rows", ctypes.c_int32), ("x_div", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("swiglu", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 EXPERT_REF_DTYPE = np.dtype([("fmt", "<u4"), ("reserved", "<u4"), ("gate", "<u8"),
@@ -119,6 +147,24 @@ def lib():
         L.moe_cpu_expert_ffn.argtypes = [dims_p, i32, vp, vp, vp, vp, i32, vp, vp, vp, i32]
         L.moe_add_chain.restype = ctypes.c_int
         L.moe_add_chain.argtypes = [vp, vp, vp, vp, i32, i32, vp]
+        gd_p, cd_p, qd_p = (ctypes.POINTER(c) for c in (GroupDims, CombineDims, Q4Dims))
+        sz_p = ctypes.POINTER(sz)
+        L.moe_group_plan_bytes.restype = sz
+        L.moe_group_plan_bytes.argtypes = [i32, i32, i32]
+        for name, args in (("moe_group_plan", [vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]),
+                           ("moe_group_matmul", [gd_p, vp, vp, vp, vp, vp, vp]),
+                           ("moe_group_swiglu", [gd_p, vp, vp, vp, vp, vp, vp, vp]),
+                           ("moe_group_matmul_t", [gd_p, vp, vp, vp, vp, vp, vp]),
+                           ("moe_group_swiglu_grad", [gd_p, vp, vp, vp, vp, vp, vp, vp]),
+                           ("moe_group_wgrad", [gd_p, vp, vp, vp, vp, vp, i32, vp]),
+                           ("moe_group_combine", [cd_p, vp, vp, vp, vp, vp]),
+                           ("moe_group_combine_grad", [cd_p, vp, vp, vp, vp, vp, vp, vp]),
+                           ("moe_q4_bytes", [i64, i64, i32, sz_p, sz_p, sz_p]),
+                           ("moe_q4_pack", [vp, i64, i64, i32, vp, vp, vp, i32]),
+                           ("moe_q4_unpack", [vp, vp, vp, i64, i64, i32, vp, i32]),
+                           ("moe_q4_matvec", [qd_p, vp, vp, vp, vp, vp, vp, vp])):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = args
         _lib = L
     return _lib
 
@@ -355,3 +401,237 @@ def moe_add_chain(y, add, noise, x_next, stream=None):
     rows, hidden = y.shape
     _check("moe_add_chain", lib().moe_add_chain(_ptr(y), _ptr(add), _ptr(noise), _ptr(x_next),
                                                 int(rows), int(hidden), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- experts at any shape
+# Shapes, strides and types are read off the tensors (torch, on the current
+# device, last dimension contiguous); what does not fit raises MoeError.
+_types = None
+
+
+def _type(fn, t):
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16}
+    code = _types.get(t.dtype)
+    if code is None:
+        raise MoeError(fn, MOE_EFORMAT)
+    return code
+
+
+def _need(fn, ok, status=MOE_ESHAPE):
+    if not ok:
+        raise MoeError(fn, status)
+
+
+def _on_device(fn, *tensors):
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise MoeError(fn, MOE_EINVAL)
+
+
+def _rows(fn, t, rows=None, cols=None):
+    """(row stride) of a 2-d tensor whose rows are contiguous."""
+    _need(fn, t.dim() == 2 and (rows is None or t.shape[0] == rows) and (cols is None or t.shape[1] == cols))
+    s0, s1 = t.stride()
+    _need(fn, s1 == 1 or t.shape[1] <= 1)
+    return s0 if t.shape[0] > 1 else max(s0, t.shape[1])
+
+
+def _ints(fn, t, n):
+    import torch
+    _need(fn, t.dtype == torch.int32, MOE_EFORMAT)
+    _need(fn, t.is_contiguous() and t.numel() == n)
+
+
+def group_plan_bytes(rows, top_k, n_groups):
+    return int(lib().moe_group_plan_bytes(int(rows), int(top_k), int(n_groups)))
+
+
+def moe_group_plan(idx, n_groups, offsets, pairs, pos, ws=None, stream=None):
+    """idx [rows, top_k] int32 -> offsets [n_groups + 1], pairs and pos [rows * top_k] (all int32);
+    ws: group_plan_bytes(rows, top_k, n_groups) bytes, or None when that is 0."""
+    fn = "moe_group_plan"
+    _on_device(fn, idx, offsets, pairs, pos, ws)
+    _need(fn, idx.dim() == 2)
+    rows, top_k = idx.shape
+    _ints(fn, idx, rows * top_k)
+    _ints(fn, offsets, n_groups + 1)
+    _ints(fn, pairs, rows * top_k)
+    _ints(fn, pos, rows * top_k)
+    _need(fn, ws is None or ws.is_contiguous())
+    _check(fn, lib().moe_group_plan(_ptr(idx), rows, top_k, int(n_groups), _ptr(offsets), _ptr(pairs), _ptr(pos),
+                                    _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _group_dims(fn, x, src, src_div, offsets, rows, w, out_type):
+    """GroupDims with everything but ldy and ld_pre, from the operand x that src selects rows of."""
+    _need(fn, w.dim() == 3)
+    groups, n, k = w.shape
+    _need(fn, (w.stride(2) == 1 or k == 1) and groups >= 1)
+    ldw = w.stride(1) if n > 1 else max(k, w.stride(1))
+    _ints(fn, offsets, groups + 1)
+    if src is not None:
+        _ints(fn, src, rows)
+    return GroupDims(groups, rows, x.shape[0], n, k, int(src_div), _type(fn, x), out_type, _rows(fn, x), 0, ldw,
+                     w.stride(0) if groups > 1 else 0, 0)
+
+
+def _product(fn, x, offsets, w, y, src, src_div, x_cols, y_cols, stream, pre=None, pre_cols=0):
+    _on_device(fn, x, offsets, w, y, src, pre)
+    _need(fn, x.dim() == 2 and y.dim() == 2 and w.dim() == 3)
+    _need(fn, x.shape[1] == x_cols and x.dtype == w.dtype)
+    rows = y.shape[0]
+    d = _group_dims(fn, x, src, src_div, offsets, rows, w, _type(fn, y))
+    d.ldy = _rows(fn, y, rows, y_cols)
+    args = [ctypes.byref(d), _ptr(x), _ptr(src), _ptr(offsets), _ptr(w)]
+    if pre_cols:
+        if pre is not None:
+            _need(fn, pre.dtype == x.dtype)
+            d.ld_pre = _rows(fn, pre, rows, pre_cols)
+        args += [_ptr(y), _ptr(pre)] if fn == "moe_group_swiglu" else [_ptr(pre), _ptr(y)]
+    else:
+        args.append(_ptr(y))
+    _check(fn, getattr(lib(), fn)(*args, _stream(stream)))
+
+
+def moe_group_matmul(x, offsets, w, y, src=None, src_div=1, stream=None):
+    """y [rows, n] = x[src // src_div] [., k] times w [groups, n, k] of each row's group, transposed."""
+    _product("moe_group_matmul", x, offsets, w, y, src, src_div, w.shape[-1], w.shape[-2], stream)
+
+
+def moe_group_swiglu(x, offsets, w, h, pre=None, src=None, src_div=1, stream=None):
+    """h [rows, n / 2] = silu(gate) * up of (gate | up) = the product with w [groups, n, k]; pre [rows, n]
+    (gate | up) in x's type, or None."""
+    n = w.shape[-2]
+    _product("moe_group_swiglu", x, offsets, w, h, src, src_div, w.shape[-1], n // 2, stream, pre, n)
+
+
+def moe_group_matmul_t(dy, offsets, w, dx, src=None, src_div=1, stream=None):
+    """dx [rows, k] = dy [., n] times w [groups, n, k] of each row's group."""
+    _product("moe_group_matmul_t", dy, offsets, w, dx, src, src_div, w.shape[-2], w.shape[-1], stream)
+
+
+def moe_group_swiglu_grad(dy, offsets, w, pre, dpre, src=None, src_div=1, stream=None):
+    """dpre [rows, 2 k]: the gradient of (gate | up) = pre [rows, 2 k] from dy [., n], the gradient of the
+    product of h = silu(gate) * up with w [groups, n, k]."""
+    _need("moe_group_swiglu_grad", pre is not None, MOE_EINVAL)
+    k = w.shape[-1]
+    _product("moe_group_swiglu_grad", dy, offsets, w, dpre, src, src_div, w.shape[-2], 2 * k, stream, pre, 2 * k)
+
+
+def moe_group_wgrad(dy, x, offsets, dw, src=None, src_div=1, accumulate=False, stream=None):
+    """dw [groups, n, k] = (or +=) dy[rows of the group]^T x[src // src_div of those rows]."""
+    fn = "moe_group_wgrad"
+    _on_device(fn, dy, x, offsets, dw, src)
+    _need(fn, dy.dim() == 2 and x.dim() == 2 and dw.dim() == 3 and dy.dtype == x.dtype)
+    rows = dy.shape[0]
+    d = _group_dims(fn, x, src, src_div, offsets, rows, dw, _type(fn, dw))
+    _need(fn, x.shape[1] == d.k)
+    d.ldy = _rows(fn, dy, rows, d.n)
+    _check(fn, lib().moe_group_wgrad(ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(src), _ptr(offsets), _ptr(dw),
+                                     int(accumulate), _stream(stream)))
+
+
+def _combine_dims(fn, o_rows, ldo, y, pos, wts, top_k, in_type, out_type):
+    rows = y.shape[0]
+    if pos is not None:
+        _ints(fn, pos, rows * top_k)
+    if wts is not None:
+        _need(fn, _type(fn, wts) == T_F32 and wts.is_contiguous() and tuple(wts.shape) == (rows, top_k))
+    return CombineDims(rows, top_k, y.shape[1], o_rows, in_type, out_type, ldo, _rows(fn, y))
+
+
+def _top_k(fn, rows, pos, wts, o, top_k):
+    if top_k is None:
+        top_k = wts.shape[-1] if wts is not None else (pos.numel() if pos is not None else o.shape[0]) // max(rows, 1)
+    return int(top_k)
+
+
+def moe_group_combine(o, pos, wts, y, top_k=None, stream=None):
+    """y [rows, n] = sum over a row's top_k pairs of wts * o[pos]; pos None: pair p is row p; wts None: 1."""
+    fn = "moe_group_combine"
+    _on_device(fn, o, pos, wts, y)
+    _need(fn, o.dim() == 2 and y.dim() == 2 and o.shape[1] == y.shape[1])
+    d = _combine_dims(fn, o.shape[0], _rows(fn, o), y, pos, wts, _top_k(fn, y.shape[0], pos, wts, o, top_k),
+                      _type(fn, o), _type(fn, y))
+    _check(fn, lib().moe_group_combine(ctypes.byref(d), _ptr(o), _ptr(pos), _ptr(wts), _ptr(y), _stream(stream)))
+
+
+def moe_group_combine_grad(dy, o, pos, wts, d_o, d_wts, top_k=None, stream=None):
+    """d_o[pos] = wts * dy (rows of d_o that no pair names stay as they were) and d_wts = <dy, o[pos]>; either
+    output may be None.  o (None without d_wts) and d_o have the same row stride."""
+    fn = "moe_group_combine_grad"
+    _on_device(fn, dy, o, pos, wts, d_o, d_wts)
+    like = d_o if d_o is not None else o
+    _need(fn, dy.dim() == 2 and like is not None and like.dim() == 2, MOE_EINVAL)
+    ldo = _rows(fn, like, cols=dy.shape[1])
+    if o is not None:
+        _need(fn, o.dtype == dy.dtype and o.shape == like.shape and _rows(fn, o) == ldo)
+    top_k = _top_k(fn, dy.shape[0], pos, wts, like, top_k if d_wts is None else d_wts.shape[-1])
+    d = _combine_dims(fn, like.shape[0], ldo, dy, pos, wts, top_k, _type(fn, dy), _type(fn, like))
+    if d_wts is not None:
+        _need(fn, o is not None, MOE_EINVAL)
+        _need(fn, _type(fn, d_wts) == T_F32 and d_wts.is_contiguous() and tuple(d_wts.shape) == (d.rows, top_k))
+    _check(fn, lib().moe_group_combine_grad(ctypes.byref(d), _ptr(dy), _ptr(o), _ptr(pos), _ptr(wts), _ptr(d_o),
+                                            _ptr(d_wts), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- 4-bit matrix-vector products
+def q4_bytes(n, k, group):
+    """(codes, scales, zeros) bytes of a packed n x k matrix."""
+    out = [ctypes.c_size_t() for _ in range(3)]
+    _check("moe_q4_bytes", lib().moe_q4_bytes(int(n), int(k), int(group), *(ctypes.byref(v) for v in out)))
+    return tuple(int(v.value) for v in out)
+
+
+def q4_pack(w, group, zeros=False, nthreads=0):
+    """fp32 [n, k] (numpy) -> (codes uint8, scales uint8, zeros uint8 or None) (numpy), via moe_q4_pack."""
+    w = np.ascontiguousarray(w, dtype=np.float32)
+    n, k = w.shape
+    nc, ns, nz = q4_bytes(n, k, group)
+    codes, scales, zr = np.empty(nc, np.uint8), np.empty(ns, np.uint8), np.empty(nz, np.uint8) if zeros else None
+    _check("moe_q4_pack", lib().moe_q4_pack(w.ctypes.data, n, k, int(group), codes.ctypes.data, scales.ctypes.data,
+                                            None if zr is None else zr.ctypes.data, int(nthreads)))
+    return codes, scales, zr
+
+
+def q4_unpack(codes, scales, zeros, n, k, group, nthreads=0):
+    bufs = [None if b is None else np.ascontiguousarray(b).view(np.uint8).reshape(-1) for b in (codes, scales, zeros)]
+    for b, need in zip(bufs, q4_bytes(n, k, group)):
+        _need("moe_q4_unpack", b is None or b.size >= need)
+    out = np.empty((n, k), np.float32)
+    _check("moe_q4_unpack", lib().moe_q4_unpack(*(None if b is None else b.ctypes.data for b in bufs), int(n), int(k),
+                                                int(group), out.ctypes.data, int(nthreads)))
+    return out
+
+
+def moe_q4_matvec(x, codes, scales, zeros, group, y, idx=None, x_div=1, swiglu=False, n_mats=None, stream=None):
+    """y[p] = W x[p // x_div] for the rows p of y, W the matrix idx.flatten()[p] (idx None: matrix 0); swiglu:
+    W = (gate | up), y = silu(gate) * up.  codes / scales / zeros (or None): the packed matrices back to back;
+    n_mats defaults to the first dimension of codes when it has more than one, else 1."""
+    fn = "moe_q4_matvec"
+    _on_device(fn, x, codes, scales, zeros, y, idx)
+    _need(fn, x.dim() == 2 and y.dim() == 2)
+    rows, k = y.shape[0], x.shape[1]
+    n = y.shape[1] * (2 if swiglu else 1)
+    if n_mats is None:
+        n_mats = codes.shape[0] if codes.dim() > 1 else 1
+    if idx is not None:
+        _ints(fn, idx, rows)
+    _need(fn, x_div >= 1 and (rows == 0 or x.shape[0] > (rows - 1) // x_div))
+    d = Q4Dims(n, k, int(group), int(n_mats), rows, int(x_div), _type(fn, x), _type(fn, y), int(bool(swiglu)),
+               _rows(fn, x), _rows(fn, y))
+    size = _q4_sizes(n, k, int(group))
+    for t, need in zip((codes, scales, zeros), size):
+        _need(fn, t is None or (t.is_contiguous() and t.numel() * t.element_size() >= need * n_mats))
+    _check(fn, lib().moe_q4_matvec(ctypes.byref(d), _ptr(x), _ptr(idx), _ptr(codes), _ptr(scales), _ptr(zeros),
+                                   _ptr(y), _stream(stream)))
+
+
+@functools.lru_cache(maxsize=256)
+def _q4_sizes(n, k, group):
+    return q4_bytes(n, k, group)

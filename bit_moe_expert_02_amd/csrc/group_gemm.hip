@@ -1,0 +1,515 @@
+// gfx950 products of rows grouped by expert (ragged groups), in bf16 or f16
+// with fp32 sums:
+//
+//   matmul, swiglu    y[i, :]  = x[src(i), :] W_g^T           contraction over k
+//   matmul_t, ..grad  dx[i, :] = dy[src(i), :] W_g            contraction over n
+//   wgrad             dW_g     = sum_i dy[i, :]^T x[src(i), :]  over the group's rows
+//
+// One kernel computes them all as D[p][q] = sum_r P[p][r] Q[q][r]: p runs along
+// the output's contiguous dimension (the matrix instruction's rows, of which a
+// lane holds four in a row: one vector store), q along its rows.  An operand
+// is "straight" when r is contiguous in memory (x, W for matmul) and "across"
+// when p or q is (W for matmul_t, both for wgrad): a straight tile lies in LDS
+// as [p][64 r], an across tile as [64 r][p], read with the transposing LDS
+// read, so no operand is transposed in memory first.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "dev_common.h"
+#include "group.h"
+
+namespace moe {
+namespace grp {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+using dev::u32x2;
+using dev::u32x4;
+#define MOE_LDS __attribute__((address_space(3)))
+
+constexpr int kRed = 64;   // contraction per step: whole 128-byte lines of a straight row
+
+enum Epilogue { kStore, kSwigluOut, kSwigluBack };
+
+struct Gemm {
+  const uint16_t *p, *q;          // the two operands
+  void* y;
+  const uint16_t* pre_in;         // kSwigluBack: (g | u)
+  uint16_t* pre_out;              // kSwigluOut: (g | u), or null
+  const int32_t* offsets;         // [groups + 1]
+  const int32_t* src;             // rows of the gathered operand, or null
+  int64_t ldp, ldq, ldy, ld_pre;
+  int64_t p_stride, y_stride;     // per group: of P (weights), of y (wgrad)
+  int groups, rows;
+  int np, nq, nr;                 // extents (nq: wgrad; nr: the products)
+  int half;                       // I of the SwiGLU calls
+  int src_rows;                   // rows that src selects from
+  uint64_t div_magic;             // floor(i / src_div) = i * magic >> 35
+  int tiles_p, tiles_q;           // tiles of an output (tiles_q: wgrad)
+  int out_type, accumulate;
+};
+
+// ---------------------------------------------------------------------------
+// types
+// ---------------------------------------------------------------------------
+template <bool BF>
+__device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <bool BF>
+__device__ __forceinline__ uint16_t to_half(float v) {
+  if constexpr (BF) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+}
+template <bool BF>
+__device__ __forceinline__ float from_half(uint16_t v) {
+  if constexpr (BF) return static_cast<float>(__builtin_bit_cast(__bf16, v));
+  else return static_cast<float>(__builtin_bit_cast(_Float16, v));
+}
+
+// Four consecutive outputs, of which `n` exist.  `wide`: the place is aligned
+// for one vector store.
+__device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v, int n, int type, bool wide, bool add) {
+  if (type == MOE_T_F32) {
+    float* o = static_cast<float*>(y) + at;
+    if (wide && n >= 4) {
+      f32x4* o4 = reinterpret_cast<f32x4*>(o);
+      *o4 = add ? *o4 + v : v;
+    } else {
+      for (int i = 0; i < 4; ++i)
+        if (i < n) o[i] = add ? o[i] + v[i] : v[i];
+    }
+    return;
+  }
+  uint16_t* o = static_cast<uint16_t*>(y) + at;
+  if (add)
+    for (int i = 0; i < 4; ++i)
+      if (i < n) v[i] += type == MOE_T_BF16 ? from_half<true>(o[i]) : from_half<false>(o[i]);
+  uint16_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = type == MOE_T_BF16 ? to_half<true>(v[i]) : to_half<false>(v[i]);
+  if (wide && n >= 4) {
+    *reinterpret_cast<u32x2*>(o) = u32x2{h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16};
+  } else {
+    for (int i = 0; i < 4; ++i)
+      if (i < n) o[i] = h[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// work items
+// ---------------------------------------------------------------------------
+struct Item {
+  int group, begin, end;   // the group's rows
+  int p0, q0;              // first column / row of the output tile (products: q0 a pair row)
+  bool any;
+};
+
+// Workgroup ids go to the eight XCDs in turn: XCD x takes the x-th eighth of
+// the items, so tiles that share an operand share an L2.
+__device__ __forceinline__ int64_t xcd_item(int64_t items) {
+  const int64_t per = (items + 7) / 8, b = blockIdx.x;
+  if ((b >> 3) >= per) return items;
+  return (b & 7) * per + (b >> 3);
+}
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Products: the tiles of group g number ceil(rows of g / BQ) * tiles_p.  Every
+// wave finds its workgroup's item by itself: each lane sums the tiles of a
+// run of groups, a scan over the lanes gives the lane that holds the item.
+template <int BP, int BQ>
+__device__ __forceinline__ Item find_rows(const Gemm& a) {
+  const int lane = threadIdx.x & 63, per = (a.groups + 63) / 64;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int g = lane * per + i;
+    if (g < a.groups) {
+      const int b = clampi(a.offsets[g], 0, a.rows), e = clampi(a.offsets[g + 1], b, a.rows);
+      mine += (e - b + BQ - 1) / BQ;
+    }
+  }
+  int64_t upto = mine;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t v = __shfl_up(upto, o, 64);
+    if (lane >= o) upto += v;
+  }
+  const int64_t items = __shfl(upto, 63, 64) * a.tiles_p;
+  Item it{};
+  const int64_t at = xcd_item(items);
+  it.any = at < items;
+  if (!it.any) return it;
+  const uint64_t over = __ballot(upto * a.tiles_p > at);
+  const int holder = __ffsll(static_cast<unsigned long long>(over)) - 1;
+  int64_t rest = at - __shfl(upto - mine, holder, 64) * a.tiles_p;
+  for (int i = 0; i < per; ++i) {
+    const int g = holder * per + i;
+    if (g >= a.groups) break;
+    const int b = clampi(a.offsets[g], 0, a.rows), e = clampi(a.offsets[g + 1], b, a.rows);
+    const int tq = (e - b + BQ - 1) / BQ;
+    if (rest < static_cast<int64_t>(tq) * a.tiles_p) {
+      // bands of eight row tiles: the tiles in flight on an XCD are then a
+      // block of rows by columns, which shares both operands
+      const int r = static_cast<int>(rest), band = r / (8 * a.tiles_p), in = r - band * 8 * a.tiles_p;
+      const int wide = tq - 8 * band < 8 ? tq - 8 * band : 8;
+      it.group = g;
+      it.begin = b;
+      it.end = e;
+      it.p0 = in / wide * BP;
+      it.q0 = b + (8 * band + in % wide) * BQ;
+      break;
+    }
+    rest -= static_cast<int64_t>(tq) * a.tiles_p;
+  }
+  it.group = dev::uniform(it.group);
+  it.begin = dev::uniform(it.begin);
+  it.end = dev::uniform(it.end);
+  it.p0 = dev::uniform(it.p0);
+  it.q0 = dev::uniform(it.q0);
+  return it;
+}
+
+// wgrad: every group has the same tiles; each XCD takes an eighth of every
+// group's, so unequal groups do not make unequal XCDs.
+template <int BP, int BQ>
+__device__ __forceinline__ Item find_matrix(const Gemm& a) {
+  const int tiles = a.tiles_p * a.tiles_q, per = (tiles + 7) / 8, b = blockIdx.x;
+  const int x = b & 7, j = b >> 3, g = j / per, t = x * per + j % per;
+  Item it{};
+  it.any = t < tiles;
+  it.group = g;
+  it.begin = clampi(a.offsets[g], 0, a.rows);
+  it.end = clampi(a.offsets[g + 1], it.begin, a.rows);
+  const int band = t / (8 * a.tiles_p), in = t - band * 8 * a.tiles_p;
+  const int wide = a.tiles_q - 8 * band < 8 ? a.tiles_q - 8 * band : 8;
+  it.p0 = in / wide * BP;
+  it.q0 = (8 * band + in % wide) * BQ;
+  return it;
+}
+
+// Row of the gathered operand for pair row i, or -1.
+__device__ __forceinline__ int64_t source_row(const Gemm& a, int i) {
+  if (!a.src) return i;
+  const int32_t s = a.src[i];
+  const int64_t r = static_cast<int64_t>((static_cast<uint64_t>(static_cast<uint32_t>(s)) * a.div_magic) >> 35);
+  return s >= 0 && r < a.src_rows ? r : -1;
+}
+
+// ---------------------------------------------------------------------------
+// LDS tiles.  Straight: [rows][64], 128-byte rows of eight 16-byte chunks,
+// chunk c of row r at place c ^ (r & 7).  Across: [64][cols], chunks of 32
+// bytes (one 16-column unit), unit u of row r at u ^ spread(r).  Both let the
+// lanes of one read touch different banks.
+// ---------------------------------------------------------------------------
+template <int B>
+__device__ __forceinline__ int spread(int r) {
+  return B >= 128 ? (r & 3) | ((r >> 3) & 1) << 2 : r & 3;
+}
+
+template <bool ACROSS, int B>
+__device__ __forceinline__ s16x8 fragment(const MOE_LDS uint8_t* tile, int at, int kk) {
+  const int l = threadIdx.x & 63;
+  if constexpr (!ACROSS) {
+    const int r = at + (l & 15), c = kk * 4 + (l >> 4);
+    return *reinterpret_cast<const MOE_LDS s16x8*>(tile + r * 128 + ((c ^ (r & 7)) * 16));
+  } else {
+    // per 16 lanes: four rows of 16 columns in, four rows of one column out
+    const int r = kk * 32 + (l >> 4) * 8 + ((l & 15) >> 2), u = at >> 4;
+    const MOE_LDS uint8_t* lo = tile + r * (B * 2) + ((u ^ spread<B>(r)) * 32) + (l & 3) * 8;
+    const int r4 = r + 4;
+    const MOE_LDS uint8_t* hi = tile + r4 * (B * 2) + ((u ^ spread<B>(r4)) * 32) + (l & 3) * 8;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)lo);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)hi);
+    return s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  }
+}
+
+// Eight elements at `ptr`, of which the first `n` exist; the rest read as 0.
+__device__ __forceinline__ u32x4 load8(const uint16_t* ptr, int n) {
+  u32x4 v{0, 0, 0, 0};
+  if (n >= 8) {
+    __builtin_memcpy(&v, ptr, 16);    // any alignment
+  } else {
+    uint16_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = i < n ? ptr[i] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = h[2 * i] | static_cast<uint32_t>(h[2 * i + 1]) << 16;
+  }
+  return v;
+}
+
+// Row of W for slot s of a P tile at column p0.  With the SwiGLU epilogue a
+// wave's slots are half gate rows, half the up rows of the same channels.
+template <int EPI, int TP>
+__device__ __forceinline__ int p_row(const Gemm& a, int p0, int s) {
+  if constexpr (EPI != kSwigluOut) return p0 + s;
+  const int ch = p0 / 2 + s / TP * (TP / 2) + s % (TP / 2);
+  if (ch >= a.half) return a.np;
+  return s % TP < TP / 2 ? ch : a.half + ch;
+}
+
+template <bool BF, int EPI, int BP, int BQ, int TP, int TQ>
+__device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&acc)[TP / 16][TQ / 16], int wp, int wq,
+                                         int q_end, void* y) {
+  const int l = threadIdx.x & 63, col = l & 15, sub = (l >> 4) * 4;
+  const bool wide = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+#pragma unroll
+  for (int j = 0; j < TQ / 16; ++j) {
+    const int q = it.q0 + wq * TQ + j * 16 + col;
+    if (q >= q_end) continue;
+    const int64_t row = static_cast<int64_t>(q) * a.ldy;
+    if constexpr (EPI == kStore) {
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i) {
+        const int p = it.p0 + wp * TP + i * 16 + sub;
+        store4(y, row + p, acc[i][j], a.np - p, a.out_type, wide, a.accumulate);
+      }
+    } else if constexpr (EPI == kSwigluOut) {
+      // gate and up of a channel are TP/32 fragments apart
+#pragma unroll
+      for (int i = 0; i < TP / 32; ++i) {
+        const int ch = it.p0 / 2 + wp * (TP / 2) + i * 16 + sub;
+        const f32x4 g = acc[i][j], u = acc[i + TP / 32][j];
+        f32x4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = g[e] / (1.0f + __expf(-g[e])) * u[e];
+        store4(y, row + ch, h, a.half - ch, a.out_type, wide, false);
+        if (a.pre_out) {
+          const int type = BF ? MOE_T_BF16 : MOE_T_F16;
+          const int64_t prow = static_cast<int64_t>(q) * a.ld_pre;
+          const bool pw = a.ld_pre % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre_out) % 8 == 0;
+          store4(a.pre_out, prow + ch, g, a.half - ch, type, pw, false);
+          store4(a.pre_out, prow + a.half + ch, u, a.half - ch, type, pw && a.half % 4 == 0, false);
+        }
+      }
+    } else {
+      const int64_t prow = static_cast<int64_t>(q) * a.ld_pre;
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i) {
+        const int p = it.p0 + wp * TP + i * 16 + sub;
+        f32x4 dg, du;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = p + e < a.np;
+          const float g = in ? from_half<BF>(a.pre_in[prow + p + e]) : 0.0f;
+          const float u = in ? from_half<BF>(a.pre_in[prow + a.np + p + e]) : 0.0f;
+          const float s = 1.0f / (1.0f + __expf(-g)), dh = acc[i][j][e];
+          dg[e] = dh * u * s * (1.0f + g * (1.0f - s));
+          du[e] = dh * g * s;
+        }
+        store4(y, row + p, dg, a.np - p, a.out_type, wide, false);
+        store4(y, row + a.np + p, du, a.np - p, a.out_type, wide && a.np % 4 == 0, false);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Any alignment, any span: tiles go through registers.
+// ---------------------------------------------------------------------------
+template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
+  constexpr int TP = BP / WP, TQ = BQ / WQ, NT = 64 * WP * WQ;
+  constexpr bool kWeight = PA && QA;   // wgrad
+  __shared__ __attribute__((aligned(16))) uint8_t lds[(BP + BQ) * 128];
+  const Item it = kWeight ? find_matrix<BP, BQ>(a) : find_rows<BP, BQ>(a);
+  if (!it.any) return;
+  const int tid = threadIdx.x, wave = dev::uniform(tid >> 6), wp = wave % WP, wq = wave / WP;
+  const int steps_over = kWeight ? it.end - it.begin : a.nr;
+  const int q_end = kWeight ? a.nq : it.end;
+  MOE_LDS uint8_t* lp = (MOE_LDS uint8_t*)lds;
+  MOE_LDS uint8_t* lq = lp + BP * 128;
+  const uint16_t* pw = a.p + (kWeight ? 0 : it.group * a.p_stride);
+  f32x4 acc[TP / 16][TQ / 16] = {};
+
+  for (int r0 = 0; r0 < steps_over; r0 += kRed) {
+    __syncthreads();
+    for (int c = tid; c < BP * 8; c += NT) {
+      u32x4 v{0, 0, 0, 0};
+      int at;
+      if constexpr (!PA) {
+        const int s = c >> 3, ch = c & 7, row = p_row<EPI, TP>(a, it.p0, s), r = r0 + ch * 8;
+        if (row < a.np && r < a.nr) v = load8(pw + row * a.ldp + r, a.nr - r);
+        at = s * 128 + ((ch ^ (s & 7)) * 16);
+      } else {
+        const int rr = c / (BP / 8), ch = c % (BP / 8), p = it.p0 + ch * 8, r = r0 + rr;
+        if (r < steps_over && p < a.np) {
+          const int64_t row = kWeight ? source_row(a, it.begin + r) : r;
+          if (row >= 0) v = load8(pw + row * a.ldp + p, a.np - p);
+        }
+        at = rr * (BP * 2) + (((ch >> 1) ^ spread<BP>(rr)) * 32) + (ch & 1) * 16;
+      }
+      *reinterpret_cast<MOE_LDS u32x4*>(lp + at) = v;
+    }
+    for (int c = tid; c < BQ * 8; c += NT) {
+      u32x4 v{0, 0, 0, 0};
+      int at;
+      if constexpr (!QA) {
+        const int s = c >> 3, ch = c & 7, q = it.q0 + s, r = r0 + ch * 8;
+        if (q < q_end && r < a.nr) {
+          const int64_t row = source_row(a, q);
+          if (row >= 0) v = load8(a.q + row * a.ldq + r, a.nr - r);
+        }
+        at = s * 128 + ((ch ^ (s & 7)) * 16);
+      } else {
+        const int rr = c / (BQ / 8), ch = c % (BQ / 8), q = it.q0 + ch * 8, r = r0 + rr;
+        if (r < steps_over && q < a.nq) v = load8(a.q + static_cast<int64_t>(it.begin + r) * a.ldq + q, a.nq - q);
+        at = rr * (BQ * 2) + (((ch >> 1) ^ spread<BQ>(rr)) * 32) + (ch & 1) * 16;
+      }
+      *reinterpret_cast<MOE_LDS u32x4*>(lq + at) = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      s16x8 fp[TP / 16], fq[TQ / 16];
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i) fp[i] = fragment<PA, BP>(lp, wp * TP + i * 16, kk);
+#pragma unroll
+      for (int j = 0; j < TQ / 16; ++j) fq[j] = fragment<QA, BQ>(lq, wq * TQ + j * 16, kk);
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ / 16; ++j) acc[i][j] = mma<BF>(fp[i], fq[j], acc[i][j]);
+    }
+  }
+  void* y = a.y;
+  if constexpr (kWeight) y = static_cast<uint8_t*>(y) + it.group * a.y_stride * (a.out_type == MOE_T_F32 ? 4 : 2);
+  epilogue<BF, EPI, BP, BQ, TP, TQ>(a, it, acc, wp, wq, q_end, y);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxGrid = 0x7fffff00;
+
+template <bool BF, bool PA, bool QA, int EPI>
+int launch(Gemm a, hipStream_t s) {
+  constexpr int BP = 64, BQ = 64;
+  a.tiles_p = (a.np + BP - 1) / BP;
+  if (EPI == kSwigluOut) a.tiles_p = (a.half + BP / 2 - 1) / (BP / 2);
+  int64_t grid;
+  if (PA && QA) {
+    a.tiles_q = (a.nq + BQ - 1) / BQ;
+    const int64_t tiles = static_cast<int64_t>(a.tiles_p) * a.tiles_q;
+    if (tiles > kMaxGrid / 8) return MOE_ESHAPE;
+    grid = (tiles + 7) / 8 * 8 * a.groups;
+  } else {
+    // a group's last row tile may be partial: at most one more each
+    const int64_t tq = a.rows / BQ + (a.rows < a.groups ? a.rows : a.groups);
+    grid = (tq * a.tiles_p + 7) / 8 * 8;
+  }
+  if (grid > kMaxGrid) return MOE_ESHAPE;
+  hipLaunchKernelGGL((k_group_any<BF, PA, QA, EPI, BP, BQ, 2, 2>), dim3(static_cast<uint32_t>(grid)), dim3(256), 0, s, a);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EDEVICE;
+}
+
+template <bool PA, bool QA, int EPI>
+int launch_type(const moe_group_dims* d, const Gemm& a, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return d->type == MOE_T_BF16 ? launch<true, PA, QA, EPI>(a, s) : launch<false, PA, QA, EPI>(a, s);
+}
+
+Gemm common(const moe_group_dims* d, const int32_t* src, const int32_t* offsets) {
+  Gemm a{};
+  a.offsets = offsets;
+  a.src = src;
+  a.groups = d->n_groups;
+  a.rows = d->rows;
+  a.src_rows = d->x_rows;
+  a.div_magic = ((1ull << 35) + d->src_div - 1) / d->src_div;
+  a.ldy = d->ldy;
+  a.ld_pre = d->ld_pre;
+  a.out_type = d->out_type;
+  return a;
+}
+
+Gemm products(const moe_group_dims* d, const void* x, const int32_t* src, const int32_t* offsets, const void* w,
+              void* y, int np, int nr) {
+  Gemm a = common(d, src, offsets);
+  a.p = static_cast<const uint16_t*>(w);
+  a.q = static_cast<const uint16_t*>(x);
+  a.y = y;
+  a.ldp = d->ldw;
+  a.ldq = d->ldx;
+  a.p_stride = d->w_stride;
+  a.np = np;
+  a.nr = nr;
+  return a;
+}
+
+}  // namespace
+}  // namespace grp
+}  // namespace moe
+
+extern "C" {
+
+using namespace moe::grp;
+
+int moe_group_matmul(const moe_group_dims* d, const void* x, const int32_t* src, const int32_t* offsets,
+                     const void* w, void* y, void* stream) {
+  if (int st = check_group(d, kMatmul, src, false)) return st;
+  if (d->rows == 0) return MOE_OK;
+  if (!x || !offsets || !w || !y) return MOE_EINVAL;
+  return launch_type<false, false, kStore>(d, products(d, x, src, offsets, w, y, d->n, d->k), stream);
+}
+
+int moe_group_swiglu(const moe_group_dims* d, const void* x, const int32_t* src, const int32_t* offsets,
+                     const void* w, void* h, void* pre, void* stream) {
+  if (int st = check_group(d, kSwiglu, src, pre)) return st;
+  if (d->rows == 0) return MOE_OK;
+  if (!x || !offsets || !w || !h) return MOE_EINVAL;
+  Gemm a = products(d, x, src, offsets, w, h, d->n, d->k);
+  a.half = d->n / 2;
+  a.pre_out = static_cast<uint16_t*>(pre);
+  return launch_type<false, false, kSwigluOut>(d, a, stream);
+}
+
+int moe_group_matmul_t(const moe_group_dims* d, const void* dy, const int32_t* src, const int32_t* offsets,
+                       const void* w, void* dx, void* stream) {
+  if (int st = check_group(d, kMatmulT, src, false)) return st;
+  if (d->rows == 0) return MOE_OK;
+  if (!dy || !offsets || !w || !dx) return MOE_EINVAL;
+  return launch_type<true, false, kStore>(d, products(d, dy, src, offsets, w, dx, d->k, d->n), stream);
+}
+
+int moe_group_swiglu_grad(const moe_group_dims* d, const void* dy, const int32_t* src, const int32_t* offsets,
+                          const void* w, const void* pre, void* dpre, void* stream) {
+  if (int st = check_group(d, kSwigluGrad, src, true)) return st;
+  if (d->rows == 0) return MOE_OK;
+  if (!dy || !offsets || !w || !pre || !dpre) return MOE_EINVAL;
+  Gemm a = products(d, dy, src, offsets, w, dpre, d->k, d->n);
+  a.half = d->k;
+  a.pre_in = static_cast<const uint16_t*>(pre);
+  return launch_type<true, false, kSwigluBack>(d, a, stream);
+}
+
+int moe_group_wgrad(const moe_group_dims* d, const void* dy, const void* x, const int32_t* src,
+                    const int32_t* offsets, void* dw, int32_t accumulate, void* stream) {
+  if (int st = check_group(d, kWgrad, src, false)) return st;
+  if (!offsets || !dw || (d->rows && (!dy || !x))) return MOE_EINVAL;
+  Gemm a = common(d, src, offsets);
+  a.p = static_cast<const uint16_t*>(x);
+  a.q = static_cast<const uint16_t*>(dy);
+  a.y = dw;
+  a.ldp = d->ldx;
+  a.ldq = d->ldy;
+  a.ldy = d->ldw;
+  a.y_stride = d->w_stride;
+  a.np = d->k;
+  a.nq = d->n;
+  a.accumulate = accumulate != 0;
+  return launch_type<true, true, kStore>(d, a, stream);
+}
+
+}  // extern "C"

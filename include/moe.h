@@ -473,6 +473,178 @@ int moe_cpu_expert_ffn(const moe_dims* dims, int32_t fmt, const void* gate, cons
 int moe_add_chain(float* y, const float* add, const float* noise, void* x_next, int32_t rows, int32_t hidden,
                   void* stream);
 
+/* ------------------------------------------------------------------------
+ * Experts at any shape, in 16 bits: dispatch, grouped products, combine, and
+ * their gradients.
+ *
+ * The fused layer above takes two shapes and its packed formats.  The calls
+ * below take any hidden and intermediate size with bf16 or f16 expert
+ * matrices, forward and backward: for the held-out errors that
+ * moe_allocate_formats needs, for tuning experts and router, and for layers
+ * of another shape.  A layer of them:
+ *     moe_group_plan     idx -> offsets, pairs, pos
+ *     moe_group_swiglu   h = silu(x W_gate^T) * (x W_up^T)   (src = pairs)
+ *     moe_group_matmul   o = h W_down^T
+ *     moe_group_combine  y[r] = sum_j w[r,j] o[pos[r,j]]
+ * and back:
+ *     moe_group_combine_grad, moe_group_swiglu_grad (through W_down and the
+ *     SwiGLU), moe_group_matmul_t (through W_gate | W_up), moe_group_wgrad
+ *     (every matrix), moe_group_combine without weights (dx of a row is the
+ *     sum of its pairs').
+ *
+ * Rows are grouped by expert: group g owns rows offsets[g] .. offsets[g+1]-1
+ * of the pair arrays (offsets on the device, ascending; each is clamped to
+ * [0, rows], a group whose end lies before its start is empty).  Rows outside
+ * every group are left as they were.  Sums are fp32 on the matrix cores and
+ * are rounded once, to the output's type; they run in a fixed order, so the
+ * same inputs give bitwise the same outputs.  No output may overlap an input.
+ * ------------------------------------------------------------------------ */
+typedef enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2 } moe_type;
+
+/* Largest number of groups (experts) of the calls below. */
+#define MOE_MAX_GROUPS 1024
+
+/* Dispatch: idx [rows x top_k] int32 (device), as moe_route gives it.
+ *   offsets  [n_groups + 1], out: pairs with an id below g
+ *   pairs    [rows x top_k], out: the pairs (row * top_k + slot) in ascending
+ *            (id, pair) order; entries past offsets[n_groups] are -1
+ *   pos      [rows x top_k], out: the place of each pair in `pairs`; -1 for an
+ *            id of -1 (a pair computed elsewhere), -2 for any other id outside
+ *            [0, n_groups) (moe_group_combine makes its row NaN)
+ *   ws       moe_group_plan_bytes bytes (NULL when that is 0); its contents
+ *            do not matter
+ * 1 <= top_k <= MOE_MAX_TOP_K, 1 <= n_groups <= MOE_MAX_GROUPS, rows * top_k
+ * below 2^31 (MOE_ESHAPE). */
+size_t moe_group_plan_bytes(int32_t rows, int32_t top_k, int32_t n_groups);
+int moe_group_plan(const int32_t* idx, int32_t rows, int32_t top_k, int32_t n_groups, int32_t* offsets,
+                   int32_t* pairs, int32_t* pos, void* ws, size_t ws_bytes, void* stream);
+
+/* Shape of a grouped product.  Matrix g is W_g [n x k] at w + g * w_stride,
+ * row stride ldw; strides are in elements, the last dimension is contiguous. */
+typedef struct {
+  int32_t n_groups;   /* 1 .. MOE_MAX_GROUPS                                    */
+  int32_t rows;       /* rows of the pair arrays (>= 0)                         */
+  int32_t x_rows;     /* rows of the operand that `src` selects from            */
+  int32_t n, k;       /* >= 1                                                   */
+  int32_t src_div;    /* 1 .. MOE_MAX_TOP_K: row i comes from row src[i] / src_div */
+  int32_t type;       /* MOE_T_BF16 or MOE_T_F16: every operand                 */
+  int32_t out_type;   /* of the output: f32, bf16 or f16                        */
+  int64_t ldx;        /* row stride of x (matmul_t, swiglu_grad: of dy)         */
+  int64_t ldy;        /* row stride of the output rows (wgrad: of dy)           */
+  int64_t ldw, w_stride;
+  int64_t ld_pre;     /* row stride of pre / of dpre's source (SwiGLU calls)    */
+} moe_group_dims;
+
+/* The pair rows of the operand x are its rows src[i] / src_div when src is
+ * given (the `pairs` of moe_group_plan with src_div = top_k: no sorted copy of
+ * x is made), else its rows i.  A src entry that names no row reads as a row
+ * of zeros.  Without src, x_rows >= rows.
+ *
+ * y [rows x n] = x [. x k] W_g^T */
+int moe_group_matmul(const moe_group_dims* d, const void* x, const int32_t* src, const int32_t* offsets,
+                     const void* w, void* y, void* stream);
+
+/* Gate and up in one product: n = 2 I, W_g = gate (I rows) then up.
+ *   h    [rows x I], out: silu(g) * u of the fp32 sums g, u
+ *   pre  [rows x 2 I] in `type`, row stride ld_pre, out, or NULL: (g | u), what
+ *        the gradient needs */
+int moe_group_swiglu(const moe_group_dims* d, const void* x, const int32_t* src, const int32_t* offsets,
+                     const void* w, void* h, void* pre, void* stream);
+
+/* Input gradient of moe_group_matmul: dx [rows x k] = dy [. x n] W_g. */
+int moe_group_matmul_t(const moe_group_dims* d, const void* dy, const int32_t* src, const int32_t* offsets,
+                       const void* w, void* dx, void* stream);
+
+/* Gradient of (g | u) from the gradient dy of the down product's output:
+ *   dh = dy [. x n] W_g  (W_g = down [n x k], k = I),  s = 1 / (1 + e^-g)
+ *   dpre [rows x 2 I] = (dh u s (1 + g (1 - s)) | dh g s)
+ *   pre  [rows x 2 I] in `type`, row stride ld_pre, as moe_group_swiglu wrote it */
+int moe_group_swiglu_grad(const moe_group_dims* d, const void* dy, const int32_t* src, const int32_t* offsets,
+                          const void* w, const void* pre, void* dpre, void* stream);
+
+/* Weight gradient: dW_g [n x k] = sum over the group's rows i of
+ * dy[i]^T x[src(i)], dy [rows x n] with row stride ldy; dw in out_type at
+ * dw + g * w_stride, row stride ldw.  An empty group's is 0.  With accumulate
+ * it is added to what dw holds (one rounding of the fp32 sum). */
+int moe_group_wgrad(const moe_group_dims* d, const void* dy, const void* x, const int32_t* src,
+                    const int32_t* offsets, void* dw, int32_t accumulate, void* stream);
+
+/* y [rows x n] = sum over j of wts[r,j] * o[pos[r,j]], j ascending, fp32 sums.
+ *   o    [o_rows x n] in `type`, row stride ldo
+ *   pos  [rows x top_k] as moe_group_plan gives it, or NULL (pair p is row p).
+ *        -1 adds nothing; any other place outside [0, o_rows) makes the row NaN
+ *   wts  [rows x top_k] fp32, or NULL (all 1: the sum of a row's input gradients) */
+typedef struct {
+  int32_t rows, top_k, n, o_rows;
+  int32_t type;       /* of o and dy: bf16, f16 or f32                          */
+  int32_t out_type;   /* of y / d_o                                             */
+  int64_t ldo, ldy;   /* row strides of o and d_o, and of y / dy                */
+} moe_combine_dims;
+int moe_group_combine(const moe_combine_dims* d, const void* o, const int32_t* pos, const float* wts, void* y,
+                      void* stream);
+
+/* Its gradients: d_o[pos[r,j]] = wts[r,j] * dy[r] (row stride ldo, out_type)
+ * and d_wts[r,j] = <dy[r], o[pos[r,j]]> (fp32; 0 where pos is -1, NaN where it
+ * is outside [0, o_rows)).  Either output may be NULL (o may be NULL when
+ * d_wts is).  Places must be distinct; rows of d_o that no place names are
+ * left as they were. */
+int moe_group_combine_grad(const moe_combine_dims* d, const void* dy, const void* o, const int32_t* pos,
+                           const float* wts, void* d_o, float* d_wts, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Matrix-vector products with 4-bit weights and group scales: the dense half
+ * of a decoder layer, or experts of any shape, for the rows of one step.
+ *
+ * W [n x k] in codes c of 4 bits: value d * (c - z), d one fp16 per `group`
+ * (32, 64 or 128) consecutive columns of a row, z = 8, or one byte 0 .. 15 per
+ * group.  k is a multiple of `group`.  Layout, in whole tiles of 16 rows by
+ * 128 columns (N = ceil(n / 16), K = ceil(k / 128); padding has code z, d 0):
+ *   codes   [N][K][4 q][16 r][4 j] 32-bit words: nibble e (bits 4e ..) of the
+ *           word (q, r, j) is row 16 N + r, column 128 K + 32 j + 8 q + e
+ *   scales  [N][128 K / group][16 r] fp16
+ *   zeros   [N][128 K / group][16 r] bytes
+ * so a wave streams 1 KiB of codes a load and each word is one operand of a
+ * matrix instruction.
+ * ------------------------------------------------------------------------ */
+/* Bytes of the three arrays (any may be NULL).  MOE_ESHAPE for n < 1, k < 1, a
+ * group that is not 32, 64 or 128 or does not divide k. */
+int moe_q4_bytes(int64_t n, int64_t k, int32_t group, size_t* codes, size_t* scales, size_t* zeros);
+
+/* Round-to-nearest packing of fp32 w [n x k] (host) in fp32 arithmetic.
+ *   zeros NULL: d = fp16(max|w| / 7), c = clamp(rint(w / d) + 8, 0, 15)
+ *   else        lo = min(w, 0), hi = max(w, 0), d = fp16((hi - lo) / 15),
+ *               z = clamp(rint(-lo / d), 0, 15), c = clamp(rint(w / d) + z, 0, 15)
+ * per group; d == 0: c = z (z = 8 without zeros, 0 with).  Host only. */
+int moe_q4_pack(const float* w, int64_t n, int64_t k, int32_t group, void* codes, void* scales, void* zeros,
+                int32_t nthreads);
+/* Exact decode to fp32 w [n x k] (host). */
+int moe_q4_unpack(const void* codes, const void* scales, const void* zeros, int64_t n, int64_t k, int32_t group,
+                  float* w, int32_t nthreads);
+
+/* Rows of one moe_q4_matvec call. */
+#define MOE_MAX_Q4_ROWS 64
+
+typedef struct {
+  int32_t n, k, group;
+  int32_t n_mats;     /* matrices back to back in each of the three arrays      */
+  int32_t rows;       /* rows of y, 0 .. MOE_MAX_Q4_ROWS                        */
+  int32_t x_div;      /* >= 1: row p of y takes row p / x_div of x              */
+  int32_t type;       /* of x: bf16 or f16                                      */
+  int32_t out_type;   /* of y                                                   */
+  int32_t swiglu;     /* 1: W is gate (n / 2 rows) then up, y = silu(g) * u
+                         [rows x n / 2]; n a multiple of 32                     */
+  int64_t ldx, ldy;   /* row strides in elements                                */
+} moe_q4_dims;
+
+/* y[p] = W_{idx[p]} x[p / x_div], fp32 sums of exact products, one rounding.
+ *   idx    [rows] int32 (device), the matrix of each row (x_div = top_k: the
+ *          idx of moe_route), or NULL: matrix 0 for every row.  -1: the row of
+ *          y is 0 (a pair computed elsewhere); any other id outside
+ *          [0, n_mats): NaN.  Rows of one matrix read it once per call.
+ *   codes, scales, zeros (or NULL): 16-byte aligned */
+int moe_q4_matvec(const moe_q4_dims* d, const void* x, const int32_t* idx, const void* codes, const void* scales,
+                  const void* zeros, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,173 @@
+"""GPU parity of the 4-bit matrix-vector product against the fp64 oracle.
+
+Tolerance per element: codes enter as 16 + c, so a row's K products are of size
+up to 31 |x| d; every addition rounds half a step of a partial sum no larger
+than sum d (47 |x|) (the start (16 + z) sum|x| included): (K + 8) * 2^-24 times
+that, plus the output's rounding.  SwiGLU as in the grouped products' tests."""
+
+import numpy as np
+import pytest
+
+from oracle import group as OG
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from bit_moe_expert_02_amd import _lib as L          # noqa: E402
+from tests.test_gpu_group import _close, _dev, _f64, _half_step, _silu_rel   # noqa: E402
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+class Weights:
+    def __init__(self, mats, n, k, group, zeros, seed=0):
+        rng = np.random.default_rng(seed + n + k)
+        self.n, self.k, self.group = n, k, group
+        self.values, self.steps, packed = [], [], []
+        for _ in range(mats):
+            w = (rng.standard_normal((n, k)) * 0.05).astype(np.float32)
+            w[0, :group] = 0
+            codes, scales, z = OG.q4_quantise(w, group, zeros)
+            self.values.append(OG.q4_values(codes, scales, z, group))
+            self.steps.append(np.repeat(scales.astype(np.float64), group, axis=1))
+            packed.append(L.q4_pack(w, group, zeros))
+        cat = lambda i: torch.from_numpy(np.stack([p[i] for p in packed])).cuda()  # noqa: E731
+        self.codes, self.scales, self.zeros = cat(0), cat(1), cat(2) if zeros else None
+
+    def product(self, x, pick, swiglu, out):
+        """(reference, tolerance) for rows x [P, k] (fp64) and matrices pick [P]."""
+        y = np.stack([self.values[m] @ v for m, v in zip(pick, x)])
+        tol = np.stack([self.steps[m] @ np.abs(v) for m, v in zip(pick, x)]) * 47 * (self.k + 8) * 2.0**-24
+        if swiglu:
+            (g, u), (tg, tu) = np.split(y, 2, 1), np.split(tol, 2, 1)
+            y = g * OG.sigmoid(g) * u
+            tol = 1.1 * tg * (np.abs(u) + tu) + np.abs(g * OG.sigmoid(g)) * tu + np.abs(y) * _silu_rel(g)
+        return y, tol + _half_step(y, out)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F16, F32), (BF16, F32)])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("n,k,group", [(16, 32, 32), (64, 128, 64), (1, 256, 128), (33, 96, 32), (512, 512, 32),
+                                       (250, 1152, 128), (96, 5120, 64), (2304, 640, 64)])
+@pytest.mark.parametrize("rows", [1, 3, 16, 17, 64])
+def test_dense(rows, n, k, group, zeros, dtype, out):
+    w = Weights(1, n, k, group, zeros)
+    rng = np.random.default_rng(rows)
+    x = _dev(rng.standard_normal((rows, k)), dtype)
+    for swiglu in ([False, True] if n % 32 == 0 else [False]):
+        y = torch.full((rows, n // 2 if swiglu else n), 7.0, dtype=out, device="cuda")
+        L.moe_q4_matvec(x, w.codes, w.scales, w.zeros, group, y, swiglu=swiglu)
+        ref, tol = w.product(_f64(x), [0] * rows, swiglu, out)
+        _close(y, ref, tol, f"swiglu {swiglu}")
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("rows,top_k,mats", [(1, 1, 1), (1, 6, 16), (8, 6, 16), (8, 8, 3), (5, 3, 128), (64, 1, 2)])
+def test_experts(rows, top_k, mats, zeros):
+    """Each pair's own matrix, several pairs of one matrix, skipped pairs and ids of no matrix."""
+    n, k, group = 96, 288, 32
+    w = Weights(mats, n, k, group, zeros, seed=mats)
+    rng = np.random.default_rng(rows * top_k)
+    idx = rng.integers(0, mats, (rows, top_k)).astype(np.int32)
+    flat = idx.reshape(-1)
+    if flat.size > 8:
+        flat[3], flat[5], flat[7] = -1, mats, -2
+    ok = (flat >= 0) & (flat < mats)
+    x = _dev(rng.standard_normal((rows, k)), BF16)
+    for swiglu in (False, True):
+        cols = n // 2 if swiglu else n
+        y = torch.full((rows * top_k, cols), 7.0, device="cuda")
+        L.moe_q4_matvec(x, w.codes, w.scales, w.zeros, group, y, idx=_dev(idx, torch.int32), x_div=top_k, swiglu=swiglu)
+        ref, tol = w.product(np.repeat(_f64(x), top_k, 0)[ok], flat[ok], swiglu, F32)
+        _close(y[torch.from_numpy(ok).cuda()], ref, tol)
+        y = y.cpu().numpy()
+        assert (y[flat == -1] == 0).all() and np.isnan(y[~ok & (flat != -1)]).all()
+    # a row of x for every pair (the down product)
+    xp = _dev(rng.standard_normal((rows * top_k, k)), F16)
+    y = torch.empty((rows * top_k, n), device="cuda")
+    L.moe_q4_matvec(xp, w.codes, w.scales, w.zeros, group, y, idx=_dev(idx, torch.int32))
+    ref, tol = w.product(_f64(xp)[ok], flat[ok], False, F32)
+    _close(y[torch.from_numpy(ok).cuda()], ref, tol)
+
+
+def test_strides_and_alignment():
+    n, k, group = 80, 160, 32
+    w = Weights(1, n, k, group, True)
+    rng = np.random.default_rng(0)
+    xs = rng.standard_normal((5, k))
+    for pad in (1, 3, 8):
+        buf = torch.full((5 * (k + pad) + 1,), float("nan"), dtype=BF16, device="cuda")
+        x = buf[1:].view(5, k + pad)[:, :k]
+        x.copy_(_dev(xs, BF16))
+        whole = torch.full((5, n + pad), 7.0, dtype=F16, device="cuda")
+        L.moe_q4_matvec(x, w.codes, w.scales, w.zeros, group, whole[:, :n])
+        ref, tol = w.product(_f64(x), [0] * 5, False, F16)
+        _close(whole[:, :n], ref, tol)
+        assert bool((whole[:, n:] == 7).all())
+
+
+def test_values_that_are_not_finite_stay_in_their_rows():
+    w = Weights(1, 48, 256, 32, False)
+    x = torch.ones((20, 256), dtype=BF16, device="cuda")
+    x[4, 100], x[17, 3] = float("nan"), float("inf")
+    y = torch.empty((20, 48), device="cuda")
+    L.moe_q4_matvec(x, w.codes, w.scales, w.zeros, 32, y)
+    fine = torch.isfinite(y).all(1).cpu().numpy()
+    assert not fine[4] and not fine[17] and fine.sum() == 18
+
+
+def test_layer_of_4_bit_experts_for_one_step():
+    """Route's idx and weights -> gate/up + SwiGLU -> down -> combine, captured and replayed."""
+    rows, top_k, mats, hidden, inter, group = 3, 2, 5, 160, 96, 32
+    w1, w2 = Weights(mats, 2 * inter, hidden, group, True), Weights(mats, hidden, inter, group, False, seed=9)
+    rng = np.random.default_rng(5)
+    x = _dev(rng.standard_normal((rows, hidden)), BF16)
+    idx = _dev(np.array([[0, 3], [3, 1], [4, 0]], np.int32), torch.int32)
+    wts = _dev(rng.random((rows, top_k)), F32)
+    h, o = torch.empty((rows * top_k, inter), dtype=F16, device="cuda"), torch.empty((rows * top_k, hidden), device="cuda")
+    y = torch.empty((rows, hidden), device="cuda")
+
+    def step():
+        L.moe_q4_matvec(x, w1.codes, w1.scales, w1.zeros, group, h, idx=idx, x_div=top_k, swiglu=True)
+        L.moe_q4_matvec(h, w2.codes, w2.scales, w2.zeros, group, o, idx=idx)
+        L.moe_group_combine(o, None, wts, y)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in range(3):
+        x.copy_(_dev(rng.standard_normal((rows, hidden)), BF16))
+        idx.copy_(_dev(rng.integers(0, mats, (rows, top_k)), torch.int32))
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        pick = idx.cpu().numpy().reshape(-1)
+        want = np.zeros((rows, hidden))
+        for p, m in enumerate(pick):
+            g, u = np.split(w1.values[m] @ _f64(x)[p // top_k], 2)
+            want[p // top_k] += float(wts.view(-1)[p]) * (w2.values[m] @ (g * OG.sigmoid(g) * u))
+        err = np.linalg.norm(_f64(y) - want) / np.linalg.norm(want)
+        assert err <= 2 * 2.0**-11, err                  # one f16 rounding, of h
+    eager = y.clone()
+    step()
+    assert torch.equal(eager, y)
+
+
+def test_binding_refuses():
+    w = Weights(2, 64, 128, 32, False)
+    x, y = torch.zeros((2, 128), dtype=BF16, device="cuda"), torch.zeros((2, 64), device="cuda")
+    bad = [lambda: L.moe_q4_matvec(x, w.codes[:, :-16], w.scales, None, 32, y), lambda: L.moe_q4_matvec(x, w.codes, w.scales, None, 48, y),
+           lambda: L.moe_q4_matvec(x.float(), w.codes, w.scales, None, 32, y), lambda: L.moe_q4_matvec(x[:1], w.codes, w.scales, None, 32, y),
+           lambda: L.moe_q4_matvec(x, w.codes, w.scales, None, 32, y, idx=torch.zeros(3, dtype=torch.int32, device="cuda")),
+           lambda: L.moe_q4_matvec(x, w.codes, w.scales, None, 32, y, n_mats=3),
+           lambda: L.moe_q4_matvec(x, w.codes, w.scales, w.codes[:, 8:72], 32, y),
+           lambda: L.moe_q4_matvec(x, w.codes, w.scales, None, 32, torch.zeros((65, 64), device="cuda"))]
+    for i, f in enumerate(bad):
+        with pytest.raises(L.MoeError):
+            f()
+            pytest.fail(f"case {i} was taken")
