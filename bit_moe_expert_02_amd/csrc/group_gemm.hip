@@ -121,6 +121,8 @@ __device__ __forceinline__ int64_t xcd_item(int64_t items) {
   return (b & 7) * per + (b >> 3);
 }
 
+__device__ __forceinline__ int wave_id() { return dev::uniform(static_cast<int>(threadIdx.x >> 6)); }
+
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 // Products: the tiles of group g number ceil(rows of g / BQ) * tiles_p.  Every
@@ -323,7 +325,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[(BP + BQ) * 128];
   const Item it = kWeight ? find_matrix<BP, BQ>(a) : find_rows<BP, BQ>(a);
   if (!it.any) return;
-  const int tid = threadIdx.x, wave = dev::uniform(tid >> 6), wp = wave % WP, wq = wave / WP;
+  const int tid = threadIdx.x, wave = wave_id(), wp = wave % WP, wq = wave / WP;
   const int steps_over = kWeight ? it.end - it.begin : a.nr;
   const int q_end = kWeight ? a.nq : it.end;
   MOE_LDS uint8_t* lp = (MOE_LDS uint8_t*)lds;
@@ -387,31 +389,222 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
 }
 
 // ---------------------------------------------------------------------------
+// Aligned operands: tiles go from memory to LDS without passing registers.
+// A buffer load writes LDS in lane order, 16 bytes a lane, so the swizzles of
+// the tiles are applied to the lanes' source addresses.  Reads outside an
+// operand (a row of no group, a row past the contraction) return zeros by the
+// buffer's bounds; kOutside is past every buffer (all are below 2 GiB).
+// ---------------------------------------------------------------------------
+constexpr uint32_t kOutside = 0x7ffffff0u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint16_t* base, int64_t rows, int64_t ld, int64_t cols) {
+  const int64_t bytes = rows > 0 ? ((rows - 1) * ld + cols) * 2 : 0;
+  void* u = reinterpret_cast<void*>(dev::uniform(reinterpret_cast<uint64_t>(base)));
+  return __builtin_amdgcn_make_buffer_rsrc(u, 0, dev::uniform(static_cast<int>(bytes)), 0x00020000);
+}
+
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t b, MOE_LDS uint8_t* at, uint32_t lane_off, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (MOE_LDS void*)at, 16, static_cast<int>(lane_off), static_cast<int>(off), 0, 0);
+}
+
+// The loads of one operand's tile: N of them a wave, 64 chunks of 16 bytes each.
+template <bool ACROSS, int B, int WAVES>
+struct Feed {
+  static constexpr int N = B / (8 * WAVES);
+  static constexpr int kRowsPerLoad = ACROSS ? 512 / B : 8;
+  __amdgpu_buffer_rsrc_t buf;
+  uint32_t lane[N];        // byte offset of each load's chunk in the first step
+  int chunk;               // straight: this lane's chunk of a row
+  int red;                 // contraction length
+  uint32_t step;           // bytes a step
+
+  // Tile row (straight: of the tile, across: of the step) that load i of this lane fetches.
+  static __device__ __forceinline__ int row(int i) {
+    const int l = threadIdx.x & 63, w = wave_id();
+    return (w * N + i) * kRowsPerLoad + (ACROSS ? l / (B / 8) : l >> 3);
+  }
+  // Across: the column of the chunk that load i of this lane fetches.
+  static __device__ __forceinline__ int col(int i) {
+    const int place = (threadIdx.x & 63) % (B / 8), u = (place >> 1) ^ spread<B>(row(i));
+    return u * 16 + (place & 1) * 8;
+  }
+  __device__ __forceinline__ void set_chunk() { chunk = (threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7); }
+
+  // Straight operands and across operands without a gather.
+  __device__ __forceinline__ void load(MOE_LDS uint8_t* tile, int t) const {
+    const int w = wave_id(), left = red - t * kRed;
+    MOE_LDS uint8_t* at = tile + w * N * 1024;
+    if (ACROSS || left >= kRed) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) to_lds(buf, at + i * 1024, lane[i], t * step);
+    } else {
+      // a straight row ends inside the step: what follows it must not be read
+#pragma unroll
+      for (int i = 0; i < N; ++i) to_lds(buf, at + i * 1024, chunk * 8 < left ? lane[i] : kOutside, t * step);
+    }
+  }
+};
+
+template <int LOADS>
+__device__ __forceinline__ void step_barrier() {
+  // this wave's loads of the step have landed and its reads of the last one
+  // are done; behind the barrier that holds for every wave
+  if constexpr (LOADS == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
+}
+
+template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ, int STAGES>
+__global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
+  constexpr int TP = BP / WP, TQ = BQ / WQ, NW = WP * WQ;
+  constexpr bool kWeight = PA && QA;   // wgrad
+  constexpr int kStage = (BP + BQ) * 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * kStage];
+  const Item it = kWeight ? find_matrix<BP, BQ>(a) : find_rows<BP, BQ>(a);
+  if (!it.any) return;
+  const int wave = wave_id(), wp = wave % WP, wq = wave / WP;
+  const int red = kWeight ? it.end - it.begin : a.nr;
+  const int q_end = kWeight ? a.nq : it.end;
+  MOE_LDS uint8_t* base = (MOE_LDS uint8_t*)lds;
+
+  Feed<PA, BP, NW> fp;
+  Feed<QA, BQ, NW> fq;
+  fp.red = fq.red = red;
+  fp.set_chunk();
+  fq.set_chunk();
+  if constexpr (!PA) {
+    fp.buf = buffer_of(a.p + it.group * a.p_stride, a.np, a.ldp, a.nr);
+    fp.step = kRed * 2;
+#pragma unroll
+    for (int i = 0; i < fp.N; ++i) {
+      const int row = p_row<EPI, TP>(a, it.p0, fp.row(i));
+      fp.lane[i] = row < a.np ? static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldp * 2) + fp.chunk * 16 : kOutside;
+    }
+  } else {
+    const bool gather = kWeight && a.src;
+    fp.buf = kWeight ? (gather ? buffer_of(a.p, a.src_rows, a.ldp, a.np) : buffer_of(a.p + it.begin * a.ldp, red, a.ldp, a.np))
+                     : buffer_of(a.p + it.group * a.p_stride, a.nr, a.ldp, a.np);
+    fp.step = static_cast<uint32_t>(kRed * 2 * a.ldp);
+#pragma unroll
+    for (int i = 0; i < fp.N; ++i)
+      fp.lane[i] = (gather ? 0u : fp.row(i) * static_cast<uint32_t>(a.ldp * 2)) + (it.p0 + fp.col(i)) * 2;
+  }
+  if constexpr (!QA) {
+    const bool gather = a.src != nullptr;
+    fq.buf = gather ? buffer_of(a.q, a.src_rows, a.ldq, a.nr) : buffer_of(a.q + it.q0 * a.ldq, it.end - it.q0, a.ldq, a.nr);
+    fq.step = kRed * 2;
+#pragma unroll
+    for (int i = 0; i < fq.N; ++i) {
+      const int r = fq.row(i);
+      int64_t row = r;
+      if (gather) row = it.q0 + r < it.end ? source_row(a, it.q0 + r) : -1;
+      fq.lane[i] = it.q0 + r < it.end && row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldq * 2) + fq.chunk * 16 : kOutside;
+    }
+  } else {
+    fq.buf = buffer_of(a.q + it.begin * a.ldq, red, a.ldq, a.nq);
+    fq.step = static_cast<uint32_t>(kRed * 2 * a.ldq);
+#pragma unroll
+    for (int i = 0; i < fq.N; ++i) fq.lane[i] = fq.row(i) * static_cast<uint32_t>(a.ldq * 2) + (it.q0 + fq.col(i)) * 2;
+  }
+
+  const auto issue = [&](int t) {
+    MOE_LDS uint8_t* tp = base + t % STAGES * kStage;
+    if (kWeight && a.src) {
+      // the rows of x follow src: one 32-bit load per row, then the chunks
+#pragma unroll
+      for (int i = 0; i < fp.N; ++i) {
+        const int r = t * kRed + fp.row(i);
+        const int64_t row = r < red ? source_row(a, it.begin + r) : -1;
+        to_lds(fp.buf, tp + (wave * fp.N + i) * 1024,
+               row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldp * 2) + fp.lane[i] : kOutside, 0);
+      }
+    } else {
+      fp.load(tp, t);
+    }
+    fq.load(tp + BP * 128, t);
+  };
+
+  f32x4 acc[TP / 16][TQ / 16] = {};
+  const int steps = (red + kRed - 1) / kRed;
+  // steps past the last read nothing (every lane is outside), so the number of
+  // loads in flight is the same at every barrier
+#pragma unroll
+  for (int t = 0; t < STAGES - 1; ++t) issue(t);
+  for (int t = 0; t < steps; ++t) {
+    step_barrier<(STAGES - 2) * (decltype(fp)::N + decltype(fq)::N)>();
+    issue(t + STAGES - 1);
+    const MOE_LDS uint8_t* lp = base + t % STAGES * kStage;
+    const MOE_LDS uint8_t* lq = lp + BP * 128;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      s16x8 vp[TP / 16], vq[TQ / 16];
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i) vp[i] = fragment<PA, BP>(lp, wp * TP + i * 16, kk);
+#pragma unroll
+      for (int j = 0; j < TQ / 16; ++j) vq[j] = fragment<QA, BQ>(lq, wq * TQ + j * 16, kk);
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ / 16; ++j) acc[i][j] = mma<BF>(vp[i], vq[j], acc[i][j]);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  void* y = a.y;
+  if constexpr (kWeight) y = static_cast<uint8_t*>(y) + it.group * a.y_stride * (a.out_type == MOE_T_F32 ? 4 : 2);
+  epilogue<BF, EPI, BP, BQ, TP, TQ>(a, it, acc, wp, wq, q_end, y);
+}
+
+// ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
 namespace {
 
 constexpr int64_t kMaxGrid = 0x7fffff00;
 
-template <bool BF, bool PA, bool QA, int EPI>
-int launch(Gemm a, hipStream_t s) {
-  constexpr int BP = 64, BQ = 64;
-  a.tiles_p = (a.np + BP - 1) / BP;
-  if (EPI == kSwigluOut) a.tiles_p = (a.half + BP / 2 - 1) / (BP / 2);
+// Whether k_group_tiles takes the operands: 16-byte aligned rows, whole
+// 16-byte chunks along a straight contraction, every buffer below 2 GiB.
+template <bool PA, bool QA>
+bool direct(const Gemm& a) {
+  constexpr int64_t kMost = 0x7fff0000;
+  const auto fits = [](int64_t rows, int64_t ld) { return (rows + 4 * kRed) * ld * 2 < kMost; };
+  if (reinterpret_cast<uintptr_t>(a.p) % 16 || reinterpret_cast<uintptr_t>(a.q) % 16) return false;
+  if (a.ldp % 8 || a.ldq % 8 || a.p_stride % 8) return false;
+  if (!QA && a.nr % 8) return false;
+  if (PA && QA) return fits(a.rows, a.ldq) && fits(a.src ? a.src_rows : a.rows, a.ldp);
+  return fits(PA ? a.nr : a.np, a.ldp) && fits(a.src ? a.src_rows : 256, a.ldq);
+}
+
+// Workgroups of a launch with tiles of BP x BQ (0: too many); fills in the tile counts.
+template <bool WEIGHT, int EPI>
+int64_t grid_of(Gemm& a, int BP, int BQ) {
+  a.tiles_p = EPI == kSwigluOut ? (a.half + BP / 2 - 1) / (BP / 2) : (a.np + BP - 1) / BP;
   int64_t grid;
-  if (PA && QA) {
+  if (WEIGHT) {
     a.tiles_q = (a.nq + BQ - 1) / BQ;
     const int64_t tiles = static_cast<int64_t>(a.tiles_p) * a.tiles_q;
-    if (tiles > kMaxGrid / 8) return MOE_ESHAPE;
+    if (tiles > kMaxGrid / 8) return 0;
     grid = (tiles + 7) / 8 * 8 * a.groups;
   } else {
     // a group's last row tile may be partial: at most one more each
     const int64_t tq = a.rows / BQ + (a.rows < a.groups ? a.rows : a.groups);
     grid = (tq * a.tiles_p + 7) / 8 * 8;
   }
-  if (grid > kMaxGrid) return MOE_ESHAPE;
-  hipLaunchKernelGGL((k_group_any<BF, PA, QA, EPI, BP, BQ, 2, 2>), dim3(static_cast<uint32_t>(grid)), dim3(256), 0, s, a);
+  return grid > kMaxGrid ? 0 : grid;
+}
+
+template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ, int STAGES>
+int go(Gemm a, hipStream_t s) {
+  const int64_t grid = grid_of<PA && QA, EPI>(a, BP, BQ);
+  if (!grid) return MOE_ESHAPE;
+  const dim3 g(static_cast<uint32_t>(grid)), b(64 * WP * WQ);
+  if constexpr (STAGES == 0) hipLaunchKernelGGL((k_group_any<BF, PA, QA, EPI, BP, BQ, WP, WQ>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((k_group_tiles<BF, PA, QA, EPI, BP, BQ, WP, WQ, STAGES>), g, b, 0, s, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EDEVICE;
+}
+
+template <bool BF, bool PA, bool QA, int EPI>
+int launch(const Gemm& a, hipStream_t s) {
+  if (!direct<PA, QA>(a)) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 0>(a, s);
+  return go<BF, PA, QA, EPI, 256, 256, 2, 4, 2>(a, s);
 }
 
 template <bool PA, bool QA, int EPI>
