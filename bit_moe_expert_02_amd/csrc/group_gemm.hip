@@ -259,58 +259,140 @@ __device__ __forceinline__ int p_row(const Gemm& a, int p0, int s) {
   return s % TP < TP / 2 ? ch : a.half + ch;
 }
 
-template <bool BF, int EPI, int BP, int BQ, int TP, int TQ>
+// Rows of 16 outputs by TP columns that a wave holds as fragments (a lane: one
+// row, four columns of each 16) go through LDS, from where a lane takes 16
+// bytes of output in a row: a wave then writes whole lines.  Storing the
+// fragments as they are writes 32-byte pieces of 16 rows at a time, which
+// took a 256 x 256 tile's product from 1141 to 1010 TFLOP/s at 8192^3.
+template <int C>
+struct Rows {
+  static constexpr int kPitch = C * 4 + 16;   // bytes; the odd 16 spread the rows over the banks
+  static constexpr int kBytes = 16 * kPitch;
+  MOE_LDS uint8_t* at;
+
+  __device__ __forceinline__ void put(int i, f32x4 v) const {
+    const int l = threadIdx.x & 63;
+    *reinterpret_cast<MOE_LDS f32x4*>(at + (l & 15) * kPitch + i * 64 + (l >> 4) * 16) = v;
+  }
+  // Columns [c0, c0 + C) of `cols` of rows q0 .. of y, as far as q_end.
+  __device__ __forceinline__ void flush(void* y, int64_t ld, int q0, int q_end, int c0, int cols, int type, bool wide,
+                                        bool add) const {
+    const int l = threadIdx.x & 63;
+    if (type == MOE_T_F32) {
+#pragma unroll
+      for (int s = 0; s < C / 16; ++s) {
+        const int r = (s * 64 + l) / (C / 4), c = (s * 64 + l) % (C / 4) * 4;
+        const f32x4 v = *reinterpret_cast<const MOE_LDS f32x4*>(at + r * kPitch + c * 4);
+        if (q0 + r < q_end) store4(y, (q0 + r) * ld + c0 + c, v, cols - c0 - c, type, wide, add);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < (C + 31) / 32; ++s) {   // the lanes past row 15 (C = 16) rest
+        const int r = (s * 64 + l) / (C / 8), c = (s * 64 + l) % (C / 8) * 8;
+        if (C < 32 && r >= 16) continue;
+        const MOE_LDS uint8_t* p = at + r * kPitch + c * 4;
+        const f32x4 lo = *reinterpret_cast<const MOE_LDS f32x4*>(p), hi = *reinterpret_cast<const MOE_LDS f32x4*>(p + 16);
+        if (q0 + r >= q_end) continue;
+        const int64_t o = (q0 + r) * ld + c0 + c;
+        if (wide && !add && c0 + c + 8 <= cols) {
+          u32x4 h;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 v = i < 2 ? lo : hi;
+            const float x0 = v[2 * (i & 1)], x1 = v[2 * (i & 1) + 1];
+            h[i] = type == MOE_T_BF16 ? to_half<true>(x0) | static_cast<uint32_t>(to_half<true>(x1)) << 16
+                                      : to_half<false>(x0) | static_cast<uint32_t>(to_half<false>(x1)) << 16;
+          }
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(y) + o) = h;
+        } else {
+          store4(y, o, lo, cols - c0 - c, type, false, add);
+          store4(y, o + 4, hi, cols - c0 - c - 4, type, false, add);
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ bool wide_rows(const void* y, int64_t ld, int type) {
+  return ld % (type == MOE_T_F32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+}
+
+// `lds`: room for a Rows<TP> a wave; every wave's tile reads are done.
+template <bool BF, int EPI, int TP, int TQ>
 __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&acc)[TP / 16][TQ / 16], int wp, int wq,
-                                         int q_end, void* y) {
-  const int l = threadIdx.x & 63, col = l & 15, sub = (l >> 4) * 4;
-  const bool wide = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+                                         int q_end, void* y, MOE_LDS uint8_t* lds) {
+  constexpr int C = EPI == kSwigluOut ? TP / 2 : TP;   // columns of an output that a wave holds
+  const int type = BF ? MOE_T_BF16 : MOE_T_F16;
+  const Rows<C> rows{lds + wave_id() * Rows<C>::kBytes};
+  const bool wide = wide_rows(y, a.ldy, a.out_type);
+  const int c0 = (EPI == kSwigluOut ? it.p0 / 2 : it.p0) + wp * C;
 #pragma unroll
   for (int j = 0; j < TQ / 16; ++j) {
-    const int q = it.q0 + wq * TQ + j * 16 + col;
-    if (q >= q_end) continue;
-    const int64_t row = static_cast<int64_t>(q) * a.ldy;
+    const int q0 = it.q0 + wq * TQ + j * 16;
+    if (q0 >= q_end) break;
     if constexpr (EPI == kStore) {
 #pragma unroll
-      for (int i = 0; i < TP / 16; ++i) {
-        const int p = it.p0 + wp * TP + i * 16 + sub;
-        store4(y, row + p, acc[i][j], a.np - p, a.out_type, wide, a.accumulate);
-      }
+      for (int i = 0; i < TP / 16; ++i) rows.put(i, acc[i][j]);
+      rows.flush(y, a.ldy, q0, q_end, c0, a.np, a.out_type, wide, a.accumulate);
     } else if constexpr (EPI == kSwigluOut) {
-      // gate and up of a channel are TP/32 fragments apart
+      // gate and up of a channel are TP / 32 fragments apart
 #pragma unroll
       for (int i = 0; i < TP / 32; ++i) {
-        const int ch = it.p0 / 2 + wp * (TP / 2) + i * 16 + sub;
         const f32x4 g = acc[i][j], u = acc[i + TP / 32][j];
         f32x4 h;
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = g[e] / (1.0f + __expf(-g[e])) * u[e];
-        store4(y, row + ch, h, a.half - ch, a.out_type, wide, false);
-        if (a.pre_out) {
-          const int type = BF ? MOE_T_BF16 : MOE_T_F16;
-          const int64_t prow = static_cast<int64_t>(q) * a.ld_pre;
-          const bool pw = a.ld_pre % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre_out) % 8 == 0;
-          store4(a.pre_out, prow + ch, g, a.half - ch, type, pw, false);
-          store4(a.pre_out, prow + a.half + ch, u, a.half - ch, type, pw && a.half % 4 == 0, false);
-        }
+        rows.put(i, h);
+      }
+      rows.flush(y, a.ldy, q0, q_end, c0, a.half, a.out_type, wide, false);
+      if (a.pre_out) {
+        const bool pw = wide_rows(a.pre_out, a.ld_pre, type);
+#pragma unroll
+        for (int i = 0; i < TP / 32; ++i) rows.put(i, acc[i][j]);
+        rows.flush(a.pre_out, a.ld_pre, q0, q_end, c0, a.half, type, pw, false);
+#pragma unroll
+        for (int i = 0; i < TP / 32; ++i) rows.put(i, acc[i + TP / 32][j]);
+        rows.flush(a.pre_out + a.half, a.ld_pre, q0, q_end, c0, a.half, type, pw && a.half % 8 == 0, false);
       }
     } else {
-      const int64_t prow = static_cast<int64_t>(q) * a.ld_pre;
+      const int l = threadIdx.x & 63, q = q0 + (l & 15), p = c0 + (l >> 4) * 4;
+      const uint16_t* gp = a.pre_in + static_cast<int64_t>(q) * a.ld_pre + p;
+      const bool pw = a.ld_pre % 4 == 0 && a.np % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre_in) % 8 == 0;
+      u32x2 gv[TP / 16], uv[TP / 16];
 #pragma unroll
       for (int i = 0; i < TP / 16; ++i) {
-        const int p = it.p0 + wp * TP + i * 16 + sub;
-        f32x4 dg, du;
+        gv[i] = uv[i] = u32x2{0, 0};
+        if (q >= q_end) continue;
+        if (pw && p + i * 16 + 4 <= a.np) {
+          gv[i] = *reinterpret_cast<const u32x2*>(gp + i * 16);
+          uv[i] = *reinterpret_cast<const u32x2*>(gp + a.np + i * 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (p + i * 16 + e < a.np) {
+              gv[i][e / 2] |= static_cast<uint32_t>(gp[i * 16 + e]) << 16 * (e & 1);
+              uv[i][e / 2] |= static_cast<uint32_t>(gp[a.np + i * 16 + e]) << 16 * (e & 1);
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i) {
+        f32x4 dg;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool in = p + e < a.np;
-          const float g = in ? from_half<BF>(a.pre_in[prow + p + e]) : 0.0f;
-          const float u = in ? from_half<BF>(a.pre_in[prow + a.np + p + e]) : 0.0f;
+          const float g = from_half<BF>(static_cast<uint16_t>(gv[i][e / 2] >> 16 * (e & 1)));
+          const float u = from_half<BF>(static_cast<uint16_t>(uv[i][e / 2] >> 16 * (e & 1)));
           const float s = 1.0f / (1.0f + __expf(-g)), dh = acc[i][j][e];
           dg[e] = dh * u * s * (1.0f + g * (1.0f - s));
-          du[e] = dh * g * s;
+          acc[i][j][e] = dh * g * s;
         }
-        store4(y, row + p, dg, a.np - p, a.out_type, wide, false);
-        store4(y, row + a.np + p, du, a.np - p, a.out_type, wide && a.np % 4 == 0, false);
+        rows.put(i, dg);
       }
+      rows.flush(y, a.ldy, q0, q_end, c0, a.np, a.out_type, wide, false);
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i) rows.put(i, acc[i][j]);
+      rows.flush(static_cast<uint8_t*>(y) + static_cast<int64_t>(a.np) * (a.out_type == MOE_T_F32 ? 4 : 2), a.ldy, q0, q_end,
+                c0, a.np, a.out_type, wide && a.np % 8 == 0, false);
     }
   }
 }
@@ -322,7 +404,8 @@ template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
   constexpr int TP = BP / WP, TQ = BQ / WQ, NT = 64 * WP * WQ;
   constexpr bool kWeight = PA && QA;   // wgrad
-  __shared__ __attribute__((aligned(16))) uint8_t lds[(BP + BQ) * 128];
+  constexpr int kTiles = (BP + BQ) * 128, kOut = WP * WQ * Rows<TP>::kBytes;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kTiles > kOut ? kTiles : kOut];
   const Item it = kWeight ? find_matrix<BP, BQ>(a) : find_rows<BP, BQ>(a);
   if (!it.any) return;
   const int tid = threadIdx.x, wave = wave_id(), wp = wave % WP, wq = wave / WP;
@@ -383,9 +466,10 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
         for (int j = 0; j < TQ / 16; ++j) acc[i][j] = mma<BF>(fp[i], fq[j], acc[i][j]);
     }
   }
+  __syncthreads();
   void* y = a.y;
   if constexpr (kWeight) y = static_cast<uint8_t*>(y) + it.group * a.y_stride * (a.out_type == MOE_T_F32 ? 4 : 2);
-  epilogue<BF, EPI, BP, BQ, TP, TQ>(a, it, acc, wp, wq, q_end, y);
+  epilogue<BF, EPI, TP, TQ>(a, it, acc, wp, wq, q_end, y, lp);
 }
 
 // ---------------------------------------------------------------------------
@@ -458,6 +542,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
   constexpr int TP = BP / WP, TQ = BQ / WQ, NW = WP * WQ;
   constexpr bool kWeight = PA && QA;   // wgrad
   constexpr int kStage = (BP + BQ) * 128;
+  static_assert(NW * Rows<TP>::kBytes <= STAGES * kStage, "the epilogue's rows use the tiles' memory");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * kStage];
   const Item it = kWeight ? find_matrix<BP, BQ>(a) : find_rows<BP, BQ>(a);
   if (!it.any) return;
@@ -524,33 +609,71 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
   };
 
   f32x4 acc[TP / 16][TQ / 16] = {};
-  const int steps = (red + kRed - 1) / kRed;
-  // steps past the last read nothing (every lane is outside), so the number of
-  // loads in flight is the same at every barrier
-#pragma unroll
-  for (int t = 0; t < STAGES - 1; ++t) issue(t);
-  for (int t = 0; t < steps; ++t) {
-    step_barrier<(STAGES - 2) * (decltype(fp)::N + decltype(fq)::N)>();
-    issue(t + STAGES - 1);
+  s16x8 vp[TP / 16], vq[TQ / 16];
+  const auto read = [&](int t, int kk) {
     const MOE_LDS uint8_t* lp = base + t % STAGES * kStage;
     const MOE_LDS uint8_t* lq = lp + BP * 128;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      s16x8 vp[TP / 16], vq[TQ / 16];
+    for (int i = 0; i < TP / 16; ++i) vp[i] = fragment<PA, BP>(lp, wp * TP + i * 16, kk);
 #pragma unroll
-      for (int i = 0; i < TP / 16; ++i) vp[i] = fragment<PA, BP>(lp, wp * TP + i * 16, kk);
+    for (int j = 0; j < TQ / 16; ++j) vq[j] = fragment<QA, BQ>(lq, wq * TQ + j * 16, kk);
+  };
+  const auto multiply = [&] {
 #pragma unroll
-      for (int j = 0; j < TQ / 16; ++j) vq[j] = fragment<QA, BQ>(lq, wq * TQ + j * 16, kk);
+    for (int i = 0; i < TP / 16; ++i)
 #pragma unroll
-      for (int i = 0; i < TP / 16; ++i)
+      for (int j = 0; j < TQ / 16; ++j) acc[i][j] = mma<BF>(vp[i], vq[j], acc[i][j]);
+  };
+  const int steps = (red + kRed - 1) / kRed;
+  if constexpr (STAGES == 2 && NW == 8) {
+    // Two waves share a SIMD, and four of the eight run one phase behind the
+    // other four: while one wave of a SIMD multiplies, the other one reads its
+    // next fragments and issues loads, so the matrix cores see no gap.  A step
+    // is four phases (read and multiply each half of the 64), with a barrier
+    // after each.  The tile of step t + 1 is loaded over that of step t - 1,
+    // whose last reader was done a phase before step t began, and has landed
+    // at the end of the fourth phase of step t: the leading waves wait there,
+    // the others in their third phase, which ends at the same barrier.
+    const bool behind = wave >= 4;
+    issue(0);
+    step_barrier<0>();
+    if (behind) asm volatile("s_barrier" ::: "memory");
+    for (int t = 0; t < steps; ++t) {
 #pragma unroll
-        for (int j = 0; j < TQ / 16; ++j) acc[i][j] = mma<BF>(vp[i], vq[j], acc[i][j]);
+      for (int kk = 0; kk < 2; ++kk) {
+        read(t, kk);
+        if (kk == 0) issue(t + 1);
+        if (kk == 1 && behind) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+        multiply();
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (kk == 1 && !behind) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_barrier" ::: "memory");
+      }
+    }
+    if (!behind) asm volatile("s_barrier" ::: "memory");
+  } else {
+    // steps past the last read nothing (every lane is outside), so the number
+    // of loads in flight is the same at every barrier
+#pragma unroll
+    for (int t = 0; t < STAGES - 1; ++t) issue(t);
+    for (int t = 0; t < steps; ++t) {
+      step_barrier<(STAGES - 2) * (decltype(fp)::N + decltype(fq)::N)>();
+      issue(t + STAGES - 1);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        read(t, kk);
+        multiply();
+      }
     }
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  step_barrier<0>();
   void* y = a.y;
   if constexpr (kWeight) y = static_cast<uint8_t*>(y) + it.group * a.y_stride * (a.out_type == MOE_T_F32 ? 4 : 2);
-  epilogue<BF, EPI, BP, BQ, TP, TQ>(a, it, acc, wp, wq, q_end, y);
+  epilogue<BF, EPI, TP, TQ>(a, it, acc, wp, wq, q_end, y, base);
 }
 
 // ---------------------------------------------------------------------------
