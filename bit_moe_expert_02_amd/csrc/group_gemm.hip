@@ -31,6 +31,8 @@ using dev::u32x2;
 using dev::u32x4;
 #define MOE_LDS __attribute__((address_space(3)))
 
+using ConstInts = const int32_t __attribute__((address_space(4)))*;   // read through scalar loads
+
 constexpr int kRed = 64;   // contraction per step: whole 128-byte lines of a straight row
 
 enum Epilogue { kStore, kSwigluOut, kSwigluBack };
@@ -48,7 +50,8 @@ struct Gemm {
   int np, nq, nr;                 // extents (nq: wgrad; nr: the products)
   int half;                       // I of the SwiGLU calls
   int src_rows;                   // rows that src selects from
-  uint64_t div_magic;             // floor(i / src_div) = i * magic >> 35
+  uint32_t div_mul;               // floor(s / src_div) = (s * div_mul) >> 32 >> div_shift; 0: src_div is 1
+  int div_shift;
   int tiles_p, tiles_q;           // tiles of an output (tiles_q: wgrad)
   int out_type, accumulate;
 };
@@ -197,13 +200,14 @@ __device__ __forceinline__ Item find_matrix(const Gemm& a) {
   return it;
 }
 
-// Row of the gathered operand for pair row i, or -1.
-__device__ __forceinline__ int64_t source_row(const Gemm& a, int i) {
-  if (!a.src) return i;
-  const int32_t s = a.src[i];
-  const int64_t r = static_cast<int64_t>((static_cast<uint64_t>(static_cast<uint32_t>(s)) * a.div_magic) >> 35);
+// Row that a src entry names, or -1.
+__device__ __forceinline__ int named_row(const Gemm& a, int32_t s) {
+  const uint32_t u = static_cast<uint32_t>(s);
+  const int r = static_cast<int>(a.div_mul ? __umulhi(u, a.div_mul) >> a.div_shift : u);
   return s >= 0 && r < a.src_rows ? r : -1;
 }
+// Row of the gathered operand for pair row i, or -1.
+__device__ __forceinline__ int source_row(const Gemm& a, int i) { return a.src ? named_row(a, a.src[i]) : i; }
 
 // ---------------------------------------------------------------------------
 // LDS tiles.  Straight: [rows][64], 128-byte rows of eight 16-byte chunks,
@@ -580,7 +584,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
 #pragma unroll
     for (int i = 0; i < fq.N; ++i) {
       const int r = fq.row(i);
-      int64_t row = r;
+      int row = r;
       if (gather) row = it.q0 + r < it.end ? source_row(a, it.q0 + r) : -1;
       fq.lane[i] = it.q0 + r < it.end && row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldq * 2) + fq.chunk * 16 : kOutside;
     }
@@ -591,17 +595,42 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
     for (int i = 0; i < fq.N; ++i) fq.lane[i] = fq.row(i) * static_cast<uint32_t>(a.ldq * 2) + (it.q0 + fq.col(i)) * 2;
   }
 
+  // wgrad: the rows of x follow src.  A load covers kR of them, the same for
+  // the whole wave, so their entries come through scalar loads (which no
+  // vector-memory count waits for), a step before they are used.
+  constexpr int kR = PA ? Feed<PA, BP, NW>::kRowsPerLoad : 1, kNext = decltype(fp)::N * kR;
+  [[maybe_unused]] int32_t next[kNext];
+  const auto fetch = [&](int t) {
+    if constexpr (kWeight) {
+      const int first = it.begin + t * kRed + wave * kNext;
+      const ConstInts src = reinterpret_cast<ConstInts>(reinterpret_cast<uintptr_t>(a.src));
+      if (first + kNext <= it.end) {
+#pragma unroll
+        for (int i = 0; i < kNext; ++i) next[i] = src[first + i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kNext; ++i) next[i] = first + i < it.end ? src[first + i] : -1;
+      }
+    }
+  };
+  if (kWeight && a.src) fetch(0);
+
   const auto issue = [&](int t) {
     MOE_LDS uint8_t* tp = base + t % STAGES * kStage;
     if (kWeight && a.src) {
-      // the rows of x follow src: one 32-bit load per row, then the chunks
+      const int sub = (threadIdx.x & 63) / (BP / 8);   // which of a load's rows
 #pragma unroll
       for (int i = 0; i < fp.N; ++i) {
-        const int r = t * kRed + fp.row(i);
-        const int64_t row = r < red ? source_row(a, it.begin + r) : -1;
-        to_lds(fp.buf, tp + (wave * fp.N + i) * 1024,
-               row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldp * 2) + fp.lane[i] : kOutside, 0);
+        uint32_t off = 0;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          const int row = named_row(a, next[i * kR + r]);
+          const uint32_t at = row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldp * 2) : kOutside;
+          off = r == 0 || sub == r ? at : off;
+        }
+        to_lds(fp.buf, tp + (wave * fp.N + i) * 1024, off + fp.lane[i], 0);
       }
+      fetch(t + 1);
     } else {
       fp.load(tp, t);
     }
@@ -743,7 +772,10 @@ Gemm common(const moe_group_dims* d, const int32_t* src, const int32_t* offsets)
   a.groups = d->n_groups;
   a.rows = d->rows;
   a.src_rows = d->x_rows;
-  a.div_magic = ((1ull << 35) + d->src_div - 1) / d->src_div;
+  // exact for entries below 2^31: with m = ceil(2^(32 + s) / d), the error of
+  // u m / 2^(32 + s) is below u / 2^(32 + s) < 1 / d, as d < 2^(s + 1) or is a power of two
+  a.div_shift = d->src_div <= 2 ? 0 : d->src_div <= 4 ? 1 : 2;
+  a.div_mul = d->src_div == 1 ? 0 : static_cast<uint32_t>(((1ull << (32 + a.div_shift)) + d->src_div - 1) / d->src_div);
   a.ldy = d->ldy;
   a.ld_pre = d->ld_pre;
   a.out_type = d->out_type;
