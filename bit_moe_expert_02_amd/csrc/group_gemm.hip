@@ -118,67 +118,80 @@ struct Item {
 
 // Workgroup ids go to the eight XCDs in turn: XCD x takes the x-th eighth of
 // the items, so tiles that share an operand share an L2.
-__device__ __forceinline__ int64_t xcd_item(int64_t items) {
-  const int64_t per = (items + 7) / 8, b = blockIdx.x;
-  if ((b >> 3) >= per) return items;
-  return (b & 7) * per + (b >> 3);
+__device__ __forceinline__ int xcd_item(int items) {
+  const int per = (items + 7) / 8, b = blockIdx.x;
+  return (b >> 3) < per ? (b & 7) * per + (b >> 3) : items;
 }
 
 __device__ __forceinline__ int wave_id() { return dev::uniform(static_cast<int>(threadIdx.x >> 6)); }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// Products: the tiles of group g number ceil(rows of g / BQ) * tiles_p.  Every
-// wave finds its workgroup's item by itself: each lane sums the tiles of a
-// run of groups, a scan over the lanes gives the lane that holds the item.
+// Sums over lanes 0 .. own, and over the wave, through in-register moves.
+template <int CTRL, int ROWMASK>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWMASK, 0xF, false);
+}
+__device__ __forceinline__ int scan_wave(int v) {
+  v = dpp_add<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8: sums along each row of 16
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);   // row_bcast 15 into rows 1 and 3
+  v = dpp_add<0x143, 0xC>(v);   // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
+// Products: group g has ceil(rows of g / BQ) row tiles, each tiles_p items.
+// Every wave finds its workgroup's item by itself, 64 groups at a time, one a
+// lane: the offsets of all of them are loaded first, then a scan over the
+// lanes gives the group that holds the item.  Each dependent load here is a
+// memory round trip before the tile's first byte is asked for.
 template <int BP, int BQ>
 __device__ __forceinline__ Item find_rows(const Gemm& a) {
-  const int lane = threadIdx.x & 63, per = (a.groups + 63) / 64;
-  int64_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int g = lane * per + i;
-    if (g < a.groups) {
-      const int b = clampi(a.offsets[g], 0, a.rows), e = clampi(a.offsets[g + 1], b, a.rows);
-      mine += (e - b + BQ - 1) / BQ;
-    }
+  constexpr int kMost = MOE_MAX_GROUPS / 64;
+  const int lane = threadIdx.x & 63, parts = (a.groups + 63) / 64;
+  int begin[kMost], end[kMost];
+#pragma unroll
+  for (int c = 0; c < kMost; ++c) {
+    if (c >= parts) break;
+    const int g = c * 64 + lane < a.groups ? c * 64 + lane : a.groups;   // past the last: begin = end
+    begin[c] = a.offsets[g];
+    end[c] = a.offsets[g < a.groups ? g + 1 : g];
   }
-  int64_t upto = mine;
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t v = __shfl_up(upto, o, 64);
-    if (lane >= o) upto += v;
+  int upto[kMost], total = 0;
+#pragma unroll
+  for (int c = 0; c < kMost; ++c) {
+    if (c >= parts) break;
+    begin[c] = clampi(begin[c], 0, a.rows);
+    end[c] = clampi(end[c], begin[c], a.rows);
+    upto[c] = total + scan_wave((end[c] - begin[c] + BQ - 1) / BQ);
+    total = __builtin_amdgcn_readlane(upto[c], 63);
   }
-  const int64_t items = __shfl(upto, 63, 64) * a.tiles_p;
   Item it{};
-  const int64_t at = xcd_item(items);
-  it.any = at < items;
+  const int at = xcd_item(total * a.tiles_p);
+  const int tile = at / a.tiles_p;
+  it.any = tile < total;
   if (!it.any) return it;
-  const uint64_t over = __ballot(upto * a.tiles_p > at);
-  const int holder = __ffsll(static_cast<unsigned long long>(over)) - 1;
-  int64_t rest = at - __shfl(upto - mine, holder, 64) * a.tiles_p;
-  for (int i = 0; i < per; ++i) {
-    const int g = holder * per + i;
-    if (g >= a.groups) break;
-    const int b = clampi(a.offsets[g], 0, a.rows), e = clampi(a.offsets[g + 1], b, a.rows);
-    const int tq = (e - b + BQ - 1) / BQ;
-    if (rest < static_cast<int64_t>(tq) * a.tiles_p) {
-      // bands of eight row tiles: the tiles in flight on an XCD are then a
-      // block of rows by columns, which shares both operands
-      const int r = static_cast<int>(rest), band = r / (8 * a.tiles_p), in = r - band * 8 * a.tiles_p;
-      const int wide = tq - 8 * band < 8 ? tq - 8 * band : 8;
-      it.group = g;
-      it.begin = b;
-      it.end = e;
-      it.p0 = in / wide * BP;
-      it.q0 = b + (8 * band + in % wide) * BQ;
-      break;
-    }
-    rest -= static_cast<int64_t>(tq) * a.tiles_p;
+#pragma unroll
+  for (int c = 0; c < kMost; ++c) {
+    if (c >= parts) break;
+    const uint64_t over = __ballot(upto[c] > tile);
+    if (!over) continue;
+    const int holder = __ffsll(static_cast<unsigned long long>(over)) - 1;
+    it.group = c * 64 + holder;
+    it.begin = __builtin_amdgcn_readlane(begin[c], holder);
+    it.end = __builtin_amdgcn_readlane(end[c], holder);
+    const int tq = (it.end - it.begin + BQ - 1) / BQ;
+    const int in = at - (__builtin_amdgcn_readlane(upto[c], holder) - tq) * a.tiles_p;
+    // bands of eight row tiles: the tiles in flight on an XCD are then a
+    // block of rows by columns, which shares both operands
+    const int band = in / (8 * a.tiles_p), rest = in - band * 8 * a.tiles_p;
+    const int wide = tq - 8 * band < 8 ? tq - 8 * band : 8;
+    it.p0 = rest / wide * BP;
+    it.q0 = it.begin + (8 * band + rest % wide) * BQ;
+    break;
   }
-  it.group = dev::uniform(it.group);
-  it.begin = dev::uniform(it.begin);
-  it.end = dev::uniform(it.end);
-  it.p0 = dev::uniform(it.p0);
-  it.q0 = dev::uniform(it.q0);
   return it;
 }
 
@@ -753,10 +766,19 @@ int go(Gemm a, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EDEVICE;
 }
 
+// FORCE
 template <bool BF, bool PA, bool QA, int EPI>
 int launch(const Gemm& a, hipStream_t s) {
   if (!direct<PA, QA>(a)) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 0>(a, s);
-  return go<BF, PA, QA, EPI, 256, 256, 2, 4, 2>(a, s);
+  constexpr int kForce = 0;
+  if constexpr (kForce == 0) return go<BF, PA, QA, EPI, 256, 256, 2, 4, 2>(a, s);
+  if constexpr (kForce == 1) return go<BF, PA, QA, EPI, 128, 128, 2, 2, 2>(a, s);
+  if constexpr (kForce == 2) return go<BF, PA, QA, EPI, 256, 64, 4, 1, 2>(a, s);
+  if constexpr (kForce == 3 && QA) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 3>(a, s);
+  if constexpr (kForce == 3 && !QA) return go<BF, PA, QA, EPI, 64, 32, 2, 2, 4>(a, s);
+  if constexpr (kForce == 4) return go<BF, PA, QA, EPI, 128, 64, 2, 2, 2>(a, s);
+  if constexpr (kForce == 5) return go<BF, PA, QA, EPI, 128, 64, 2, 2, 3>(a, s);
+  if constexpr (kForce == 6) return go<BF, PA, QA, EPI, 256, 128, 4, 2, 2>(a, s);
 }
 
 template <bool PA, bool QA, int EPI>
