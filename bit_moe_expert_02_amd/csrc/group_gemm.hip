@@ -78,14 +78,18 @@ __device__ __forceinline__ float from_half(uint16_t v) {
   else return static_cast<float>(__builtin_bit_cast(_Float16, v));
 }
 
-// Four consecutive outputs, of which `n` exist.  `wide`: the place is aligned
-// for one vector store.
-__device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v, int n, int type, bool wide, bool add) {
+// Four consecutive outputs, of which `n` exist.  Whole pieces go out as one
+// vector, from any element boundary.
+__device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v, int n, int type, bool add) {
   if (type == MOE_T_F32) {
     float* o = static_cast<float*>(y) + at;
-    if (wide && n >= 4) {
-      f32x4* o4 = reinterpret_cast<f32x4*>(o);
-      *o4 = add ? *o4 + v : v;
+    if (n >= 4) {
+      if (add) {
+        f32x4 held;
+        __builtin_memcpy(&held, o, 16);
+        v += held;
+      }
+      __builtin_memcpy(o, &v, 16);
     } else {
       for (int i = 0; i < 4; ++i)
         if (i < n) o[i] = add ? o[i] + v[i] : v[i];
@@ -99,8 +103,8 @@ __device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v, int n, int 
   uint16_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = type == MOE_T_BF16 ? to_half<true>(v[i]) : to_half<false>(v[i]);
-  if (wide && n >= 4) {
-    *reinterpret_cast<u32x2*>(o) = u32x2{h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16};
+  if (n >= 4) {
+    __builtin_memcpy(o, h, 8);
   } else {
     for (int i = 0; i < 4; ++i)
       if (i < n) o[i] = h[i];
@@ -292,15 +296,14 @@ struct Rows {
     *reinterpret_cast<MOE_LDS f32x4*>(at + (l & 15) * kPitch + i * 64 + (l >> 4) * 16) = v;
   }
   // Columns [c0, c0 + C) of `cols` of rows q0 .. of y, as far as q_end.
-  __device__ __forceinline__ void flush(void* y, int64_t ld, int q0, int q_end, int c0, int cols, int type, bool wide,
-                                        bool add) const {
+  __device__ __forceinline__ void flush(void* y, int64_t ld, int q0, int q_end, int c0, int cols, int type, bool add) const {
     const int l = threadIdx.x & 63;
     if (type == MOE_T_F32) {
 #pragma unroll
       for (int s = 0; s < C / 16; ++s) {
         const int r = (s * 64 + l) / (C / 4), c = (s * 64 + l) % (C / 4) * 4;
         const f32x4 v = *reinterpret_cast<const MOE_LDS f32x4*>(at + r * kPitch + c * 4);
-        if (q0 + r < q_end) store4(y, (q0 + r) * ld + c0 + c, v, cols - c0 - c, type, wide, add);
+        if (q0 + r < q_end) store4(y, (q0 + r) * ld + c0 + c, v, cols - c0 - c, type, add);
       }
     } else {
 #pragma unroll
@@ -311,28 +314,22 @@ struct Rows {
         const f32x4 lo = *reinterpret_cast<const MOE_LDS f32x4*>(p), hi = *reinterpret_cast<const MOE_LDS f32x4*>(p + 16);
         if (q0 + r >= q_end) continue;
         const int64_t o = (q0 + r) * ld + c0 + c;
-        if (wide && !add && c0 + c + 8 <= cols) {
-          u32x4 h;
+        if (!add && c0 + c + 8 <= cols) {
+          uint16_t h[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x4 v = i < 2 ? lo : hi;
-            const float x0 = v[2 * (i & 1)], x1 = v[2 * (i & 1) + 1];
-            h[i] = type == MOE_T_BF16 ? to_half<true>(x0) | static_cast<uint32_t>(to_half<true>(x1)) << 16
-                                      : to_half<false>(x0) | static_cast<uint32_t>(to_half<false>(x1)) << 16;
+          for (int i = 0; i < 8; ++i) {
+            const float x = i < 4 ? lo[i] : hi[i - 4];
+            h[i] = type == MOE_T_BF16 ? to_half<true>(x) : to_half<false>(x);
           }
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(y) + o) = h;
+          __builtin_memcpy(static_cast<uint16_t*>(y) + o, h, 16);   // from any 2-byte boundary
         } else {
-          store4(y, o, lo, cols - c0 - c, type, false, add);
-          store4(y, o + 4, hi, cols - c0 - c - 4, type, false, add);
+          store4(y, o, lo, cols - c0 - c, type, add);
+          store4(y, o + 4, hi, cols - c0 - c - 4, type, add);
         }
       }
     }
   }
 };
-
-__device__ __forceinline__ bool wide_rows(const void* y, int64_t ld, int type) {
-  return ld % (type == MOE_T_F32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
-}
 
 // `lds`: room for a Rows<TP> a wave; every wave's tile reads are done.
 template <bool BF, int EPI, int TP, int TQ>
@@ -341,7 +338,6 @@ __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&
   constexpr int C = EPI == kSwigluOut ? TP / 2 : TP;   // columns of an output that a wave holds
   const int type = BF ? MOE_T_BF16 : MOE_T_F16;
   const Rows<C> rows{lds + wave_id() * Rows<C>::kBytes};
-  const bool wide = wide_rows(y, a.ldy, a.out_type);
   const int c0 = (EPI == kSwigluOut ? it.p0 / 2 : it.p0) + wp * C;
 #pragma unroll
   for (int j = 0; j < TQ / 16; ++j) {
@@ -350,7 +346,7 @@ __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&
     if constexpr (EPI == kStore) {
 #pragma unroll
       for (int i = 0; i < TP / 16; ++i) rows.put(i, acc[i][j]);
-      rows.flush(y, a.ldy, q0, q_end, c0, a.np, a.out_type, wide, a.accumulate);
+      rows.flush(y, a.ldy, q0, q_end, c0, a.np, a.out_type, a.accumulate);
     } else if constexpr (EPI == kSwigluOut) {
       // gate and up of a channel are TP / 32 fragments apart
 #pragma unroll
@@ -361,28 +357,26 @@ __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&
         for (int e = 0; e < 4; ++e) h[e] = g[e] / (1.0f + __expf(-g[e])) * u[e];
         rows.put(i, h);
       }
-      rows.flush(y, a.ldy, q0, q_end, c0, a.half, a.out_type, wide, false);
+      rows.flush(y, a.ldy, q0, q_end, c0, a.half, a.out_type, false);
       if (a.pre_out) {
-        const bool pw = wide_rows(a.pre_out, a.ld_pre, type);
 #pragma unroll
         for (int i = 0; i < TP / 32; ++i) rows.put(i, acc[i][j]);
-        rows.flush(a.pre_out, a.ld_pre, q0, q_end, c0, a.half, type, pw, false);
+        rows.flush(a.pre_out, a.ld_pre, q0, q_end, c0, a.half, type, false);
 #pragma unroll
         for (int i = 0; i < TP / 32; ++i) rows.put(i, acc[i + TP / 32][j]);
-        rows.flush(a.pre_out + a.half, a.ld_pre, q0, q_end, c0, a.half, type, pw && a.half % 8 == 0, false);
+        rows.flush(a.pre_out + a.half, a.ld_pre, q0, q_end, c0, a.half, type, false);
       }
     } else {
       const int l = threadIdx.x & 63, q = q0 + (l & 15), p = c0 + (l >> 4) * 4;
       const uint16_t* gp = a.pre_in + static_cast<int64_t>(q) * a.ld_pre + p;
-      const bool pw = a.ld_pre % 4 == 0 && a.np % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre_in) % 8 == 0;
       u32x2 gv[TP / 16], uv[TP / 16];
 #pragma unroll
       for (int i = 0; i < TP / 16; ++i) {
         gv[i] = uv[i] = u32x2{0, 0};
         if (q >= q_end) continue;
-        if (pw && p + i * 16 + 4 <= a.np) {
-          gv[i] = *reinterpret_cast<const u32x2*>(gp + i * 16);
-          uv[i] = *reinterpret_cast<const u32x2*>(gp + a.np + i * 16);
+        if (p + i * 16 + 4 <= a.np) {
+          __builtin_memcpy(&gv[i], gp + i * 16, 8);
+          __builtin_memcpy(&uv[i], gp + a.np + i * 16, 8);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -405,71 +399,104 @@ __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&
         }
         rows.put(i, dg);
       }
-      rows.flush(y, a.ldy, q0, q_end, c0, a.np, a.out_type, wide, false);
+      rows.flush(y, a.ldy, q0, q_end, c0, a.np, a.out_type, false);
 #pragma unroll
       for (int i = 0; i < TP / 16; ++i) rows.put(i, acc[i][j]);
       rows.flush(static_cast<uint8_t*>(y) + static_cast<int64_t>(a.np) * (a.out_type == MOE_T_F32 ? 4 : 2), a.ldy, q0, q_end,
-                c0, a.np, a.out_type, wide && a.np % 8 == 0, false);
+                c0, a.np, a.out_type, false);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Any alignment, any span: tiles go through registers.
+// Any alignment, any span: tiles go through registers.  The next step's chunks
+// (eight elements, loaded from any 2-byte boundary) are in flight while the
+// present step is multiplied.  Only the last step of a contraction and the
+// chunks that a matrix's edge cuts are read element by element.
 // ---------------------------------------------------------------------------
 template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
   constexpr int TP = BP / WP, TQ = BQ / WQ, NT = 64 * WP * WQ;
-  constexpr bool kWeight = PA && QA;   // wgrad
+  constexpr int NP = BP * 8 / NT, NQ = BQ * 8 / NT;   // chunks a thread
+  constexpr bool kWeight = PA && QA;                  // wgrad
   constexpr int kTiles = (BP + BQ) * 128, kOut = WP * WQ * Rows<TP>::kBytes;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kTiles > kOut ? kTiles : kOut];
   const Item it = kWeight ? find_matrix<BP, BQ>(a) : find_rows<BP, BQ>(a);
   if (!it.any) return;
   const int tid = threadIdx.x, wave = wave_id(), wp = wave % WP, wq = wave / WP;
-  const int steps_over = kWeight ? it.end - it.begin : a.nr;
+  const int red = kWeight ? it.end - it.begin : a.nr;
   const int q_end = kWeight ? a.nq : it.end;
   MOE_LDS uint8_t* lp = (MOE_LDS uint8_t*)lds;
   MOE_LDS uint8_t* lq = lp + BP * 128;
-  const uint16_t* pw = a.p + (kWeight ? 0 : it.group * a.p_stride);
   f32x4 acc[TP / 16][TQ / 16] = {};
 
-  for (int r0 = 0; r0 < steps_over; r0 += kRed) {
-    __syncthreads();
-    for (int c = tid; c < BP * 8; c += NT) {
-      u32x4 v{0, 0, 0, 0};
-      int at;
+  // Straight: a chunk's row stays the same.  Rows outside read as zeros.
+  const uint16_t *ps[NP], *qs[NQ];
+  if constexpr (!PA) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = tid + i * NT, row = p_row<EPI, TP>(a, it.p0, c >> 3);
+      ps[i] = row < a.np ? a.p + it.group * a.p_stride + row * a.ldp + (c & 7) * 8 : nullptr;
+    }
+  }
+  if constexpr (!QA) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int c = tid + i * NT, q = it.q0 + (c >> 3), row = q < q_end ? source_row(a, q) : -1;
+      qs[i] = row >= 0 ? a.q + row * a.ldq + (c & 7) * 8 : nullptr;
+    }
+  }
+  const auto straight = [&](const uint16_t* s, int chunk, int r0) -> u32x4 {
+    if (!s) return u32x4{0, 0, 0, 0};
+    return load8(s + r0, red - r0 - chunk * 8);
+  };
+  const auto across = [&](const uint16_t* base, int64_t ld, int r, int64_t row, int col, int cols) -> u32x4 {
+    if (r >= red || row < 0) return u32x4{0, 0, 0, 0};
+    return load8(base + row * ld + col, cols - col);
+  };
+
+  u32x4 vp[NP], vq[NQ];
+  const auto fetch = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = tid + i * NT;
       if constexpr (!PA) {
-        const int s = c >> 3, ch = c & 7, row = p_row<EPI, TP>(a, it.p0, s), r = r0 + ch * 8;
-        if (row < a.np && r < a.nr) v = load8(pw + row * a.ldp + r, a.nr - r);
-        at = s * 128 + ((ch ^ (s & 7)) * 16);
+        vp[i] = straight(ps[i], c & 7, r0);
       } else {
-        const int rr = c / (BP / 8), ch = c % (BP / 8), p = it.p0 + ch * 8, r = r0 + rr;
-        if (r < steps_over && p < a.np) {
-          const int64_t row = kWeight ? source_row(a, it.begin + r) : r;
-          if (row >= 0) v = load8(pw + row * a.ldp + p, a.np - p);
-        }
-        at = rr * (BP * 2) + (((ch >> 1) ^ spread<BP>(rr)) * 32) + (ch & 1) * 16;
+        const int r = r0 + c / (BP / 8);
+        const int64_t row = !kWeight ? r : r < red ? source_row(a, it.begin + r) : -1;
+        vp[i] = across(kWeight ? a.p : a.p + it.group * a.p_stride, a.ldp, r, row, it.p0 + c % (BP / 8) * 8, a.np);
       }
-      *reinterpret_cast<MOE_LDS u32x4*>(lp + at) = v;
     }
-    for (int c = tid; c < BQ * 8; c += NT) {
-      u32x4 v{0, 0, 0, 0};
-      int at;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int c = tid + i * NT;
       if constexpr (!QA) {
-        const int s = c >> 3, ch = c & 7, q = it.q0 + s, r = r0 + ch * 8;
-        if (q < q_end && r < a.nr) {
-          const int64_t row = source_row(a, q);
-          if (row >= 0) v = load8(a.q + row * a.ldq + r, a.nr - r);
-        }
-        at = s * 128 + ((ch ^ (s & 7)) * 16);
+        vq[i] = straight(qs[i], c & 7, r0);
       } else {
-        const int rr = c / (BQ / 8), ch = c % (BQ / 8), q = it.q0 + ch * 8, r = r0 + rr;
-        if (r < steps_over && q < a.nq) v = load8(a.q + static_cast<int64_t>(it.begin + r) * a.ldq + q, a.nq - q);
-        at = rr * (BQ * 2) + (((ch >> 1) ^ spread<BQ>(rr)) * 32) + (ch & 1) * 16;
+        const int r = r0 + c / (BQ / 8);
+        vq[i] = across(a.q, a.ldq, r, it.begin + r, it.q0 + c % (BQ / 8) * 8, a.nq);
       }
-      *reinterpret_cast<MOE_LDS u32x4*>(lq + at) = v;
+    }
+  };
+
+  fetch(0);
+  for (int r0 = 0; r0 < red; r0 += kRed) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = tid + i * NT, r = c / (PA ? BP / 8 : 8), ch = c % (PA ? BP / 8 : 8);
+      const int at = PA ? r * (BP * 2) + (((ch >> 1) ^ spread<BP>(r)) * 32) + (ch & 1) * 16 : r * 128 + ((ch ^ (r & 7)) * 16);
+      *reinterpret_cast<MOE_LDS u32x4*>(lp + at) = vp[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int c = tid + i * NT, r = c / (QA ? BQ / 8 : 8), ch = c % (QA ? BQ / 8 : 8);
+      const int at = QA ? r * (BQ * 2) + (((ch >> 1) ^ spread<BQ>(r)) * 32) + (ch & 1) * 16 : r * 128 + ((ch ^ (r & 7)) * 16);
+      *reinterpret_cast<MOE_LDS u32x4*>(lq + at) = vq[i];
     }
     __syncthreads();
+    if (r0 + kRed < red) fetch(r0 + kRed);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       s16x8 fp[TP / 16], fq[TQ / 16];
@@ -766,19 +793,89 @@ int go(Gemm a, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EDEVICE;
 }
 
-// FORCE
+// Tile shapes.  A large tile asks least of the caches per product and runs the
+// matrix cores best; small ones fill the chip with few rows or columns, keep
+// more bytes in flight per compute unit when the weights' bytes bound the
+// call, and end a step sooner when one tile's chain of steps does.  The
+// shape is chosen by a model of the time:
+//     max(compute, bytes) + min(compute, bytes) / 4
+//     compute = rounds * fixed + steps * max(rounds * latency, tiles * step)
+//     bytes   = touched weights / bandwidth
+// with `tiles` per compute unit and `rounds` = tiles / (workgroups that fit).
+// Its constants (us, us, us, -, TB/s) are fits to a sweep of every shape over
+// 24 sizes, 1 .. 16384 rows in 1 .. 384 groups; measured, us (bf16):
+//     rows x n x k (groups)      256x256  128x128  128x64   64x32
+//     64 x 4096 x 4096 (1)            78       41      37      19
+//     512 x 4096 x 4096 (1)           81       43      39      46
+//     8192 x 2304 x 5120 (8)         272      238     283     481
+//     16384 x 2304 x 5120 (16)       422      433     556    1028
+//     12288 x 2304 x 5120 (384)     2134     1731    1731    1971
+// and for weight gradients (64x64 in the last column)
+//     8192 x 1024 x 1024 (1)         178      122     100      85
+//     16384 x 5120 x 2304 (16)       441      525     587     728
+struct TileCost {
+  int bp, bq;
+  double fixed, latency, step;
+  int fit;
+  double bandwidth;
+};
+enum { kLarge, kMedium, kFlat, kSmall };
+constexpr TileCost kStraightCost[] = {{256, 256, 10, 1.15, 1.5, 1, 4.4}, {128, 128, 8, 0.58, 0.537, 2, 5.3},
+                                      {128, 64, 4, 0.5, 0.33, 3, 5.0}, {64, 32, 3, 0.25, 0.144, 3, 5.3}};
+constexpr TileCost kAcrossCost[] = {{256, 256, 10, 1.25, 1.4, 1, 4.2}, {128, 128, 8, 0.82, 0.62, 2, 5.0},
+                                    {128, 64, 4, 0.67, 0.36, 3, 4.8}, {64, 32, 3, 0.5, 0.21, 3, 4.5}};
+constexpr TileCost kWeightCost[] = {{256, 256, 10, 1.25, 1.6, 1, 5.0}, {128, 128, 8, 0.85, 0.75, 2, 5.0},
+                                    {128, 64, 4, 0.75, 0.42, 3, 5.0}, {64, 64, 3, 0.63, 0.25, 5, 5.0}};
+
+template <bool PA, bool QA, int EPI>
+int tile_shape(const Gemm& a) {
+  constexpr bool kWeight = PA && QA;
+  const double held = a.rows < a.groups ? a.rows : a.groups;   // groups with rows, at most
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const TileCost& c = kWeight ? kWeightCost[i] : PA ? kAcrossCost[i] : kStraightCost[i];
+    const double tp = EPI == kSwigluOut ? (2 * a.half + c.bp - 1) / c.bp : (a.np + c.bp - 1) / c.bp;
+    double tiles, steps, bytes;
+    if (kWeight) {
+      tiles = a.groups * tp * ((a.nq + c.bq - 1) / c.bq);
+      steps = held ? a.rows / held / kRed + 0.5 : 0.0;
+      bytes = 0.0;
+    } else {
+      // a group's last row tile is half empty in the mean; each row tile past
+      // a group's first reads its weights again, mostly from the caches
+      double tq = a.groups == 1 ? (a.rows + c.bq - 1) / c.bq : a.rows / static_cast<double>(c.bq) + held / 2;
+      tq = tq > held ? tq : held;
+      tiles = tq * tp;
+      steps = (a.nr + kRed - 1) / kRed;
+      bytes = held * a.np * a.nr * 2e-6 / c.bandwidth * (0.75 + 0.25 * tq / held);
+    }
+    const double per_cu = __builtin_ceil(tiles / 256), rounds = __builtin_ceil(per_cu / c.fit);
+    const double chain = rounds * c.latency, work = per_cu * c.step;
+    double t = rounds * c.fixed + steps * (chain > work ? chain : work);
+    // weight gradients: the tiles of a group with four times the mean rows end last
+    if (kWeight && a.groups > 1) t += 3 * steps * c.latency;
+    t = t > bytes ? t + bytes / 4 : bytes + t / 4;
+    if (i == 0 || t < least) {
+      best = i;
+      least = t;
+    }
+  }
+  return best;
+}
+
 template <bool BF, bool PA, bool QA, int EPI>
 int launch(const Gemm& a, hipStream_t s) {
-  if (!direct<PA, QA>(a)) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 0>(a, s);
-  constexpr int kForce = 0;
-  if constexpr (kForce == 0) return go<BF, PA, QA, EPI, 256, 256, 2, 4, 2>(a, s);
-  if constexpr (kForce == 1) return go<BF, PA, QA, EPI, 128, 128, 2, 2, 2>(a, s);
-  if constexpr (kForce == 2) return go<BF, PA, QA, EPI, 256, 64, 4, 1, 2>(a, s);
-  if constexpr (kForce == 3 && QA) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 3>(a, s);
-  if constexpr (kForce == 3 && !QA) return go<BF, PA, QA, EPI, 64, 32, 2, 2, 4>(a, s);
-  if constexpr (kForce == 4) return go<BF, PA, QA, EPI, 128, 64, 2, 2, 2>(a, s);
-  if constexpr (kForce == 5) return go<BF, PA, QA, EPI, 128, 64, 2, 2, 3>(a, s);
-  if constexpr (kForce == 6) return go<BF, PA, QA, EPI, 256, 128, 4, 2, 2>(a, s);
+  constexpr int kForceAny = 0;
+  if (!direct<PA, QA>(a)) { if constexpr (kForceAny == 0) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 0>(a, s); else return go<BF, PA, QA, EPI, 128, 128, 2, 2, 0>(a, s); }
+  switch (tile_shape<PA, QA, EPI>(a)) {
+    case kLarge: return go<BF, PA, QA, EPI, 256, 256, 2, 4, 2>(a, s);
+    case kMedium: return go<BF, PA, QA, EPI, 128, 128, 2, 2, 2>(a, s);
+    case kFlat: return go<BF, PA, QA, EPI, 128, 64, 2, 2, 2>(a, s);
+    default:
+      if constexpr (PA && QA) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 2>(a, s);
+      else return go<BF, PA, QA, EPI, 64, 32, 2, 2, 4>(a, s);
+  }
 }
 
 template <bool PA, bool QA, int EPI>
