@@ -255,17 +255,21 @@ __device__ __forceinline__ s16x8 fragment(const MOE_LDS uint8_t* tile, int at, i
   }
 }
 
-// Eight elements at `ptr`, of which the first `n` exist; the rest read as 0.
-__device__ __forceinline__ u32x4 load8(const uint16_t* ptr, int n) {
+// Eight elements at `ptr`, of which the first `n` are wanted and the rest read
+// as 0.  One load from any 2-byte boundary: what follows the wanted ones lies
+// inside the operand, except at its very end (`end`), where the elements are
+// read one by one.
+__device__ __forceinline__ u32x4 load8(const uint16_t* ptr, const uint16_t* end, int n) {
   u32x4 v{0, 0, 0, 0};
-  if (n >= 8) {
-    __builtin_memcpy(&v, ptr, 16);    // any alignment
-  } else {
-    uint16_t h[8];
+  if (n > 0 && ptr + 8 <= end) {
+    __builtin_memcpy(&v, ptr, 16);
+    if (n < 8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = i < n ? ptr[i] : 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = h[2 * i] | static_cast<uint32_t>(h[2 * i + 1]) << 16;
+      for (int i = 0; i < 4; ++i) v[i] = n >= 2 * i + 2 ? v[i] : n == 2 * i + 1 ? v[i] & 0xFFFFu : 0u;
+    }
+  } else if (n > 0) {
+    for (int i = 0; i < 8; ++i)
+      if (i < n) v[i / 2] |= static_cast<uint32_t>(ptr[i]) << 16 * (i & 1);
   }
   return v;
 }
@@ -411,8 +415,7 @@ __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&
 // ---------------------------------------------------------------------------
 // Any alignment, any span: tiles go through registers.  The next step's chunks
 // (eight elements, loaded from any 2-byte boundary) are in flight while the
-// present step is multiplied.  Only the last step of a contraction and the
-// chunks that a matrix's edge cuts are read element by element.
+// present step is multiplied.
 // ---------------------------------------------------------------------------
 template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
@@ -430,52 +433,90 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
   MOE_LDS uint8_t* lq = lp + BP * 128;
   f32x4 acc[TP / 16][TQ / 16] = {};
 
-  // Straight: a chunk's row stays the same.  Rows outside read as zeros.
+  const bool gather = kWeight && a.src;   // of P
+  // one past the operands' last elements
+  const uint16_t* pbase = kWeight ? a.p : a.p + it.group * a.p_stride;
+  const uint16_t* pend = pbase + (kWeight ? static_cast<int64_t>(a.src_rows) - 1 : PA ? a.nr - 1 : a.np - 1) * a.ldp + (PA ? a.np : a.nr);
+  const uint16_t* qend = a.q + (static_cast<int64_t>(kWeight ? a.rows : a.src_rows) - 1) * a.ldq + (QA ? a.nq : a.nr);
+  if constexpr (kWeight) {
+    if (!gather) pbase += it.begin * a.ldp;
+  }
+  const uint16_t* qbase = QA ? a.q + it.begin * a.ldq : a.q;
+
+  // Each chunk's place in the first step.  Straight: rows past the tile's last
+  // read another row instead (they belong to no output), entries that name no
+  // row read as zeros.
   const uint16_t *ps[NP], *qs[NQ];
-  if constexpr (!PA) {
+  uint32_t none = 0;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int c = tid + i * NT, row = p_row<EPI, TP>(a, it.p0, c >> 3);
-      ps[i] = row < a.np ? a.p + it.group * a.p_stride + row * a.ldp + (c & 7) * 8 : nullptr;
+  for (int i = 0; i < NP; ++i) {
+    const int c = tid + i * NT;
+    if constexpr (!PA) {
+      const int row = p_row<EPI, TP>(a, it.p0, c >> 3);
+      ps[i] = pbase + (row < a.np ? row : 0) * a.ldp + (c & 7) * 8;
+    } else {
+      ps[i] = pbase + c / (BP / 8) * a.ldp + it.p0 + c % (BP / 8) * 8;
     }
   }
-  if constexpr (!QA) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int c = tid + i * NT, q = it.q0 + (c >> 3), row = q < q_end ? source_row(a, q) : -1;
-      qs[i] = row >= 0 ? a.q + row * a.ldq + (c & 7) * 8 : nullptr;
+  for (int i = 0; i < NQ; ++i) {
+    const int c = tid + i * NT;
+    if constexpr (!QA) {
+      const int q = it.q0 + (c >> 3), row = source_row(a, q < q_end ? q : it.q0);
+      none |= row < 0 ? 1u << i : 0u;
+      qs[i] = qbase + (row < 0 ? 0 : row) * a.ldq + (c & 7) * 8;
+    } else {
+      qs[i] = qbase + c / (BQ / 8) * a.ldq + it.q0 + c % (BQ / 8) * 8;
     }
   }
-  const auto straight = [&](const uint16_t* s, int chunk, int r0) -> u32x4 {
-    if (!s) return u32x4{0, 0, 0, 0};
-    return load8(s + r0, red - r0 - chunk * 8);
-  };
-  const auto across = [&](const uint16_t* base, int64_t ld, int r, int64_t row, int col, int cols) -> u32x4 {
-    if (r >= red || row < 0) return u32x4{0, 0, 0, 0};
-    return load8(base + row * ld + col, cols - col);
-  };
 
   u32x4 vp[NP], vq[NQ];
   const auto fetch = [&](int r0) {
+    // A step whose chunks all lie inside their operands needs no care.  An
+    // across chunk may run past its row there: the columns past the last
+    // belong to no output.
+    const bool inner = r0 + kRed <= red && (!PA || (!gather && pbase + (r0 + kRed - 1) * a.ldp + it.p0 + BP <= pend)) &&
+                       (!QA || qbase + (r0 + kRed - 1) * a.ldq + it.q0 + BQ <= qend);
+    const int64_t po = PA ? r0 * a.ldp : r0, qo = QA ? r0 * a.ldq : r0;
+    if (inner) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int c = tid + i * NT;
-      if constexpr (!PA) {
-        vp[i] = straight(ps[i], c & 7, r0);
-      } else {
-        const int r = r0 + c / (BP / 8);
-        const int64_t row = !kWeight ? r : r < red ? source_row(a, it.begin + r) : -1;
-        vp[i] = across(kWeight ? a.p : a.p + it.group * a.p_stride, a.ldp, r, row, it.p0 + c % (BP / 8) * 8, a.np);
+      for (int i = 0; i < NP; ++i) __builtin_memcpy(&vp[i], ps[i] + po, 16);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) __builtin_memcpy(&vq[i], qs[i] + qo, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int c = tid + i * NT;
+        if constexpr (!PA) {
+          vp[i] = load8(ps[i] + po, pend, red - r0 - (c & 7) * 8);
+        } else {
+          const int r = r0 + c / (BP / 8), cols = a.np - it.p0 - c % (BP / 8) * 8;
+          const uint16_t* s = ps[i] + po;
+          bool in = r < red;
+          if (gather) {
+            const int row = in ? source_row(a, it.begin + r) : -1;
+            in = row >= 0;
+            s = pbase + row * a.ldp + a.np - cols;
+          }
+          vp[i] = load8(s, pend, !in ? 0 : s + 8 <= pend ? 8 : cols);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int c = tid + i * NT;
+        if constexpr (!QA) {
+          vq[i] = load8(qs[i] + qo, qend, red - r0 - (c & 7) * 8);
+        } else {
+          const uint16_t* s = qs[i] + qo;
+          vq[i] = load8(s, qend, r0 + c / (BQ / 8) >= red ? 0 : s + 8 <= qend ? 8 : a.nq - it.q0 - c % (BQ / 8) * 8);
+        }
       }
     }
+    if constexpr (!QA) {
+      if (a.src) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int c = tid + i * NT;
-      if constexpr (!QA) {
-        vq[i] = straight(qs[i], c & 7, r0);
-      } else {
-        const int r = r0 + c / (BQ / 8);
-        vq[i] = across(a.q, a.ldq, r, it.begin + r, it.q0 + c % (BQ / 8) * 8, a.nq);
+        for (int i = 0; i < NQ; ++i)
+          if (none >> i & 1) vq[i] = u32x4{0, 0, 0, 0};
       }
     }
   };
@@ -827,14 +868,20 @@ constexpr TileCost kAcrossCost[] = {{256, 256, 10, 1.25, 1.4, 1, 4.2}, {128, 128
 constexpr TileCost kWeightCost[] = {{256, 256, 10, 1.25, 1.6, 1, 5.0}, {128, 128, 8, 0.85, 0.75, 2, 5.0},
                                     {128, 64, 4, 0.75, 0.42, 3, 5.0}, {64, 64, 3, 0.63, 0.25, 5, 5.0}};
 
-template <bool PA, bool QA, int EPI>
-int tile_shape(const Gemm& a) {
+// The register path, any operands:
+//     8192 x 2303 x 5121 (8)         128x128 353, 64x64 599; gradients 343 / 560 and 317 / 511
+//     512 x 4097 x 4097 (1)          69, 67
+//     4096 x 511 x 513 (16), wgrad   33, 25
+constexpr TileCost kAnyCost[] = {{128, 128, 5, 0.95, 0.87, 2, 3.6}, {64, 64, 3, 0.65, 0.38, 7, 3.6}};
+
+template <bool PA, bool QA, int EPI, int N>
+int tile_shape(const Gemm& a, const TileCost (&costs)[N]) {
   constexpr bool kWeight = PA && QA;
   const double held = a.rows < a.groups ? a.rows : a.groups;   // groups with rows, at most
   int best = 0;
   double least = 0;
-  for (int i = 0; i < 4; ++i) {
-    const TileCost& c = kWeight ? kWeightCost[i] : PA ? kAcrossCost[i] : kStraightCost[i];
+  for (int i = 0; i < N; ++i) {
+    const TileCost& c = costs[i];
     const double tp = EPI == kSwigluOut ? (2 * a.half + c.bp - 1) / c.bp : (a.np + c.bp - 1) / c.bp;
     double tiles, steps, bytes;
     if (kWeight) {
@@ -866,9 +913,11 @@ int tile_shape(const Gemm& a) {
 
 template <bool BF, bool PA, bool QA, int EPI>
 int launch(const Gemm& a, hipStream_t s) {
-  constexpr int kForceAny = 0;
-  if (!direct<PA, QA>(a)) { if constexpr (kForceAny == 0) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 0>(a, s); else return go<BF, PA, QA, EPI, 128, 128, 2, 2, 0>(a, s); }
-  switch (tile_shape<PA, QA, EPI>(a)) {
+  if (!direct<PA, QA>(a)) {
+    if (tile_shape<PA, QA, EPI>(a, kAnyCost) == 0) return go<BF, PA, QA, EPI, 128, 128, 2, 2, 0>(a, s);
+    return go<BF, PA, QA, EPI, 64, 64, 2, 2, 0>(a, s);
+  }
+  switch (tile_shape<PA, QA, EPI>(a, PA && QA ? kWeightCost : PA ? kAcrossCost : kStraightCost)) {
     case kLarge: return go<BF, PA, QA, EPI, 256, 256, 2, 4, 2>(a, s);
     case kMedium: return go<BF, PA, QA, EPI, 128, 128, 2, 2, 2>(a, s);
     case kFlat: return go<BF, PA, QA, EPI, 128, 64, 2, 2, 2>(a, s);
