@@ -252,9 +252,13 @@ def _ptr(t):
 
 
 def _stream(stream):
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the handle alone: 0.1 us instead of 3
+    if raw is None:
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(raw(torch.cuda.current_device()))
 
 
 def moe_route(d, x, rows, w_router, bias, idx, wts, ws, stream=None):
@@ -405,17 +409,21 @@ def moe_add_chain(y, add, noise, x_next, stream=None):
 
 # ----------------------------------------------------------------------------- experts at any shape
 # Shapes, strides and types are read off the tensors (torch, on the current
-# device, last dimension contiguous); what does not fit raises MoeError.
-_types = None
+# device, last dimension contiguous); what does not fit raises MoeError.  A
+# small call is bound by this module, so each check is made once.
+_types = {}
+
+
+def _type_of(t):
+    if not _types:
+        import torch
+        _types.update({torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16, torch.int32: -1})
+    return _types.get(t.dtype)
 
 
 def _type(fn, t):
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16}
-    code = _types.get(t.dtype)
-    if code is None:
+    code = _type_of(t)
+    if code is None or code < 0:
         raise MoeError(fn, MOE_EFORMAT)
     return code
 
@@ -425,26 +433,39 @@ def _need(fn, ok, status=MOE_ESHAPE):
         raise MoeError(fn, status)
 
 
-def _on_device(fn, *tensors):
-    import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+def _addresses(fn, *tensors):
+    """Addresses of tensors (None: None) that have to lie on the current device."""
+    dev = tensors[0].get_device()
+    if dev >= 0:
+        import torch
+        if dev != torch.cuda.current_device():
+            dev = -1
+    out = []
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is None:
+            out.append(None)
+            continue
+        if dev < 0 or t.get_device() != dev:
             raise MoeError(fn, MOE_EINVAL)
+        out.append(t.data_ptr())
+    return out
 
 
-def _rows(fn, t, rows=None, cols=None):
-    """(row stride) of a 2-d tensor whose rows are contiguous."""
-    _need(fn, t.dim() == 2 and (rows is None or t.shape[0] == rows) and (cols is None or t.shape[1] == cols))
-    s0, s1 = t.stride()
-    _need(fn, s1 == 1 or t.shape[1] <= 1)
-    return s0 if t.shape[0] > 1 else max(s0, t.shape[1])
+def _rows(fn, t):
+    """(rows, columns, row stride) of a 2-d tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise MoeError(fn, MOE_ESHAPE)
+    (r, c), (ld, one) = t.shape, t.stride()
+    if one != 1 and c > 1:
+        raise MoeError(fn, MOE_ESHAPE)
+    return r, c, ld if r > 1 else max(ld, c)
 
 
 def _ints(fn, t, n):
-    import torch
-    _need(fn, t.dtype == torch.int32, MOE_EFORMAT)
-    _need(fn, t.is_contiguous() and t.numel() == n)
+    if _type_of(t) != -1:
+        raise MoeError(fn, MOE_EFORMAT)
+    if t.numel() != n or not t.is_contiguous():
+        raise MoeError(fn, MOE_ESHAPE)
 
 
 def group_plan_bytes(rows, top_k, n_groups):
@@ -455,129 +476,134 @@ def moe_group_plan(idx, n_groups, offsets, pairs, pos, ws=None, stream=None):
     """idx [rows, top_k] int32 -> offsets [n_groups + 1], pairs and pos [rows * top_k] (all int32);
     ws: group_plan_bytes(rows, top_k, n_groups) bytes, or None when that is 0."""
     fn = "moe_group_plan"
-    _on_device(fn, idx, offsets, pairs, pos, ws)
+    at = _addresses(fn, idx, offsets, pairs, pos, ws)
     _need(fn, idx.dim() == 2)
     rows, top_k = idx.shape
-    _ints(fn, idx, rows * top_k)
-    _ints(fn, offsets, n_groups + 1)
-    _ints(fn, pairs, rows * top_k)
-    _ints(fn, pos, rows * top_k)
+    n = rows * top_k
+    for t, count in ((idx, n), (offsets, n_groups + 1), (pairs, n), (pos, n)):
+        _ints(fn, t, count)
     _need(fn, ws is None or ws.is_contiguous())
-    _check(fn, lib().moe_group_plan(_ptr(idx), rows, top_k, int(n_groups), _ptr(offsets), _ptr(pairs), _ptr(pos),
-                                    _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+    _check(fn, lib().moe_group_plan(at[0], rows, top_k, int(n_groups), at[1], at[2], at[3], at[4],
+                                    0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def _group_dims(fn, x, src, src_div, offsets, rows, w, out_type):
-    """GroupDims with everything but ldy and ld_pre, from the operand x that src selects rows of."""
-    _need(fn, w.dim() == 3)
-    groups, n, k = w.shape
-    _need(fn, (w.stride(2) == 1 or k == 1) and groups >= 1)
-    ldw = w.stride(1) if n > 1 else max(k, w.stride(1))
+    """(GroupDims with everything but ldy and ld_pre, columns of x), x the operand that src selects rows of."""
+    kind = _type(fn, x)
+    if w.dim() != 3:
+        raise MoeError(fn, MOE_ESHAPE)
+    (groups, n, k), (stride, ldw, one) = w.shape, w.stride()
+    if groups < 1 or (one != 1 and k > 1):
+        raise MoeError(fn, MOE_ESHAPE)
     _ints(fn, offsets, groups + 1)
     if src is not None:
         _ints(fn, src, rows)
-    return GroupDims(groups, rows, x.shape[0], n, k, int(src_div), _type(fn, x), out_type, _rows(fn, x), 0, ldw,
-                     w.stride(0) if groups > 1 else 0, 0)
+    x_rows, x_cols, ldx = _rows(fn, x)
+    return GroupDims(groups, rows, x_rows, n, k, src_div, kind, out_type, ldx, 0, ldw if n > 1 else max(k, ldw),
+                     stride if groups > 1 else 0, 0), x_cols
 
 
-def _product(fn, x, offsets, w, y, src, src_div, x_cols, y_cols, stream, pre=None, pre_cols=0):
-    _on_device(fn, x, offsets, w, y, src, pre)
-    _need(fn, x.dim() == 2 and y.dim() == 2 and w.dim() == 3)
-    _need(fn, x.shape[1] == x_cols and x.dtype == w.dtype)
-    rows = y.shape[0]
-    d = _group_dims(fn, x, src, src_div, offsets, rows, w, _type(fn, y))
-    d.ldy = _rows(fn, y, rows, y_cols)
-    args = [ctypes.byref(d), _ptr(x), _ptr(src), _ptr(offsets), _ptr(w)]
-    if pre_cols:
-        if pre is not None:
-            _need(fn, pre.dtype == x.dtype)
-            d.ld_pre = _rows(fn, pre, rows, pre_cols)
-        args += [_ptr(y), _ptr(pre)] if fn == "moe_group_swiglu" else [_ptr(pre), _ptr(y)]
+def _product(fn, call, x, offsets, w, y, src, src_div, back, stream, pre=None, factor=None):
+    """factor: None without pre, else the columns of (y, pre) per column of the product, times two."""
+    xa, oa, wa, ya, sa, pa = _addresses(fn, x, offsets, w, y, src, pre)
+    rows, y_cols, ldy = _rows(fn, y)
+    d, x_cols = _group_dims(fn, x, src, src_div, offsets, rows, w, _type(fn, y))
+    d.ldy = ldy
+    x_want, cols = (d.n, d.k) if back else (d.k, d.n)
+    if x.dtype != w.dtype or x_cols != x_want or 2 * y_cols != cols * (factor[0] if factor else 2):
+        raise MoeError(fn, MOE_ESHAPE)
+    d_ref = ctypes.byref(d)
+    if factor is None:
+        st = call(d_ref, xa, sa, oa, wa, ya, _stream(stream))
     else:
-        args.append(_ptr(y))
-    _check(fn, getattr(lib(), fn)(*args, _stream(stream)))
+        if pre is not None:
+            p_rows, p_cols, d.ld_pre = _rows(fn, pre)
+            if pre.dtype != x.dtype or p_rows != rows or 2 * p_cols != cols * factor[1]:
+                raise MoeError(fn, MOE_ESHAPE)
+        st = call(d_ref, xa, sa, oa, wa, pa, ya, _stream(stream)) if back else \
+            call(d_ref, xa, sa, oa, wa, ya, pa, _stream(stream))
+    _check(fn, st)
 
 
 def moe_group_matmul(x, offsets, w, y, src=None, src_div=1, stream=None):
     """y [rows, n] = x[src // src_div] [., k] times w [groups, n, k] of each row's group, transposed."""
-    _product("moe_group_matmul", x, offsets, w, y, src, src_div, w.shape[-1], w.shape[-2], stream)
+    _product("moe_group_matmul", lib().moe_group_matmul, x, offsets, w, y, src, src_div, False, stream)
 
 
 def moe_group_swiglu(x, offsets, w, h, pre=None, src=None, src_div=1, stream=None):
     """h [rows, n / 2] = silu(gate) * up of (gate | up) = the product with w [groups, n, k]; pre [rows, n]
     (gate | up) in x's type, or None."""
-    n = w.shape[-2]
-    _product("moe_group_swiglu", x, offsets, w, h, src, src_div, w.shape[-1], n // 2, stream, pre, n)
+    _product("moe_group_swiglu", lib().moe_group_swiglu, x, offsets, w, h, src, src_div, False, stream, pre, (1, 2))
 
 
 def moe_group_matmul_t(dy, offsets, w, dx, src=None, src_div=1, stream=None):
     """dx [rows, k] = dy [., n] times w [groups, n, k] of each row's group."""
-    _product("moe_group_matmul_t", dy, offsets, w, dx, src, src_div, w.shape[-2], w.shape[-1], stream)
+    _product("moe_group_matmul_t", lib().moe_group_matmul_t, dy, offsets, w, dx, src, src_div, True, stream)
 
 
 def moe_group_swiglu_grad(dy, offsets, w, pre, dpre, src=None, src_div=1, stream=None):
     """dpre [rows, 2 k]: the gradient of (gate | up) = pre [rows, 2 k] from dy [., n], the gradient of the
     product of h = silu(gate) * up with w [groups, n, k]."""
     _need("moe_group_swiglu_grad", pre is not None, MOE_EINVAL)
-    k = w.shape[-1]
-    _product("moe_group_swiglu_grad", dy, offsets, w, dpre, src, src_div, w.shape[-2], 2 * k, stream, pre, 2 * k)
+    _product("moe_group_swiglu_grad", lib().moe_group_swiglu_grad, dy, offsets, w, dpre, src, src_div, True, stream, pre,
+             (4, 4))
 
 
 def moe_group_wgrad(dy, x, offsets, dw, src=None, src_div=1, accumulate=False, stream=None):
     """dw [groups, n, k] = (or +=) dy[rows of the group]^T x[src // src_div of those rows]."""
     fn = "moe_group_wgrad"
-    _on_device(fn, dy, x, offsets, dw, src)
-    _need(fn, dy.dim() == 2 and x.dim() == 2 and dw.dim() == 3 and dy.dtype == x.dtype)
-    rows = dy.shape[0]
-    d = _group_dims(fn, x, src, src_div, offsets, rows, dw, _type(fn, dw))
-    _need(fn, x.shape[1] == d.k)
-    d.ldy = _rows(fn, dy, rows, d.n)
-    _check(fn, lib().moe_group_wgrad(ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(src), _ptr(offsets), _ptr(dw),
-                                     int(accumulate), _stream(stream)))
+    dya, xa, oa, dwa, sa = _addresses(fn, dy, x, offsets, dw, src)
+    rows, n, ldy = _rows(fn, dy)
+    d, x_cols = _group_dims(fn, x, src, src_div, offsets, rows, dw, _type(fn, dw))
+    d.ldy = ldy
+    if dy.dtype != x.dtype or x_cols != d.k or n != d.n:
+        raise MoeError(fn, MOE_ESHAPE)
+    _check(fn, lib().moe_group_wgrad(ctypes.byref(d), dya, xa, sa, oa, dwa, 1 if accumulate else 0, _stream(stream)))
 
 
 def _combine_dims(fn, o_rows, ldo, y, pos, wts, top_k, in_type, out_type):
-    rows = y.shape[0]
+    rows, n, ldy = _rows(fn, y)
     if pos is not None:
         _ints(fn, pos, rows * top_k)
-    if wts is not None:
-        _need(fn, _type(fn, wts) == T_F32 and wts.is_contiguous() and tuple(wts.shape) == (rows, top_k))
-    return CombineDims(rows, top_k, y.shape[1], o_rows, in_type, out_type, ldo, _rows(fn, y))
+    if wts is not None and (_type(fn, wts) != T_F32 or wts.shape != (rows, top_k) or not wts.is_contiguous()):
+        raise MoeError(fn, MOE_ESHAPE)
+    return CombineDims(rows, top_k, n, o_rows, in_type, out_type, ldo, ldy)
 
 
-def _top_k(fn, rows, pos, wts, o, top_k):
+def _top_k(fn, rows, pos, wts, o_rows, top_k):
     if top_k is None:
-        top_k = wts.shape[-1] if wts is not None else (pos.numel() if pos is not None else o.shape[0]) // max(rows, 1)
+        top_k = wts.shape[-1] if wts is not None else (pos.numel() if pos is not None else o_rows) // max(rows, 1)
     return int(top_k)
 
 
 def moe_group_combine(o, pos, wts, y, top_k=None, stream=None):
     """y [rows, n] = sum over a row's top_k pairs of wts * o[pos]; pos None: pair p is row p; wts None: 1."""
     fn = "moe_group_combine"
-    _on_device(fn, o, pos, wts, y)
-    _need(fn, o.dim() == 2 and y.dim() == 2 and o.shape[1] == y.shape[1])
-    d = _combine_dims(fn, o.shape[0], _rows(fn, o), y, pos, wts, _top_k(fn, y.shape[0], pos, wts, o, top_k),
-                      _type(fn, o), _type(fn, y))
-    _check(fn, lib().moe_group_combine(ctypes.byref(d), _ptr(o), _ptr(pos), _ptr(wts), _ptr(y), _stream(stream)))
+    oa, pa, wa, ya = _addresses(fn, o, pos, wts, y)
+    kind, out = _type(fn, o), _type(fn, y)
+    o_rows, n, ldo = _rows(fn, o)
+    d = _combine_dims(fn, o_rows, ldo, y, pos, wts, _top_k(fn, y.shape[0], pos, wts, o_rows, top_k), kind, out)
+    _need(fn, d.n == n)
+    _check(fn, lib().moe_group_combine(ctypes.byref(d), oa, pa, wa, ya, _stream(stream)))
 
 
 def moe_group_combine_grad(dy, o, pos, wts, d_o, d_wts, top_k=None, stream=None):
     """d_o[pos] = wts * dy (rows of d_o that no pair names stay as they were) and d_wts = <dy, o[pos]>; either
     output may be None.  o (None without d_wts) and d_o have the same row stride."""
     fn = "moe_group_combine_grad"
-    _on_device(fn, dy, o, pos, wts, d_o, d_wts)
+    dya, oa, pa, wa, doa, dwa = _addresses(fn, dy, o, pos, wts, d_o, d_wts)
     like = d_o if d_o is not None else o
-    _need(fn, dy.dim() == 2 and like is not None and like.dim() == 2, MOE_EINVAL)
-    ldo = _rows(fn, like, cols=dy.shape[1])
+    _need(fn, like is not None and (d_wts is None or o is not None), MOE_EINVAL)
+    kind, out = _type(fn, dy), _type(fn, like)
+    o_rows, n, ldo = _rows(fn, like)
     if o is not None:
-        _need(fn, o.dtype == dy.dtype and o.shape == like.shape and _rows(fn, o) == ldo)
-    top_k = _top_k(fn, dy.shape[0], pos, wts, like, top_k if d_wts is None else d_wts.shape[-1])
-    d = _combine_dims(fn, like.shape[0], ldo, dy, pos, wts, top_k, _type(fn, dy), _type(fn, like))
+        _need(fn, o.dtype == dy.dtype and _rows(fn, o) == (o_rows, n, ldo))
+    top_k = _top_k(fn, dy.shape[0], pos, wts, o_rows, top_k if d_wts is None else d_wts.shape[-1])
+    d = _combine_dims(fn, o_rows, ldo, dy, pos, wts, top_k, kind, out)
+    _need(fn, d.n == n)
     if d_wts is not None:
-        _need(fn, o is not None, MOE_EINVAL)
-        _need(fn, _type(fn, d_wts) == T_F32 and d_wts.is_contiguous() and tuple(d_wts.shape) == (d.rows, top_k))
-    _check(fn, lib().moe_group_combine_grad(ctypes.byref(d), _ptr(dy), _ptr(o), _ptr(pos), _ptr(wts), _ptr(d_o),
-                                            _ptr(d_wts), _stream(stream)))
+        _need(fn, _type(fn, d_wts) == T_F32 and d_wts.is_contiguous() and d_wts.shape == (d.rows, top_k))
+    _check(fn, lib().moe_group_combine_grad(ctypes.byref(d), dya, oa, pa, wa, doa, dwa, _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- 4-bit matrix-vector products
@@ -614,22 +640,22 @@ def moe_q4_matvec(x, codes, scales, zeros, group, y, idx=None, x_div=1, swiglu=F
     W = (gate | up), y = silu(gate) * up.  codes / scales / zeros (or None): the packed matrices back to back;
     n_mats defaults to the first dimension of codes when it has more than one, else 1."""
     fn = "moe_q4_matvec"
-    _on_device(fn, x, codes, scales, zeros, y, idx)
-    _need(fn, x.dim() == 2 and y.dim() == 2)
-    rows, k = y.shape[0], x.shape[1]
-    n = y.shape[1] * (2 if swiglu else 1)
+    xa, ca, sa, za, ya, ia = _addresses(fn, x, codes, scales, zeros, y, idx)
+    kind, out = _type(fn, x), _type(fn, y)
+    x_rows, k, ldx = _rows(fn, x)
+    rows, n, ldy = _rows(fn, y)
+    if swiglu:
+        n *= 2
     if n_mats is None:
         n_mats = codes.shape[0] if codes.dim() > 1 else 1
     if idx is not None:
         _ints(fn, idx, rows)
-    _need(fn, x_div >= 1 and (rows == 0 or x.shape[0] > (rows - 1) // x_div))
-    d = Q4Dims(n, k, int(group), int(n_mats), rows, int(x_div), _type(fn, x), _type(fn, y), int(bool(swiglu)),
-               _rows(fn, x), _rows(fn, y))
-    size = _q4_sizes(n, k, int(group))
-    for t, need in zip((codes, scales, zeros), size):
-        _need(fn, t is None or (t.is_contiguous() and t.numel() * t.element_size() >= need * n_mats))
-    _check(fn, lib().moe_q4_matvec(ctypes.byref(d), _ptr(x), _ptr(idx), _ptr(codes), _ptr(scales), _ptr(zeros),
-                                   _ptr(y), _stream(stream)))
+    _need(fn, x_div >= 1 and (rows == 0 or x_rows > (rows - 1) // x_div))
+    for t, need in zip((codes, scales, zeros), _q4_sizes(n, k, group)):
+        if t is not None and (t.numel() * t.element_size() < need * n_mats or not t.is_contiguous()):
+            raise MoeError(fn, MOE_ESHAPE)
+    d = Q4Dims(n, k, group, n_mats, rows, x_div, kind, out, 1 if swiglu else 0, ldx, ldy)
+    _check(fn, lib().moe_q4_matvec(ctypes.byref(d), xa, ia, ca, sa, za, ya, _stream(stream)))
 
 
 @functools.lru_cache(maxsize=256)
