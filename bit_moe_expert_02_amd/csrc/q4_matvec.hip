@@ -26,8 +26,24 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 using dev::u32x4;
+#define MOE_Q4_LDS __attribute__((address_space(3)))
 
-constexpr int kQ4Waves = 4;
+// A workgroup of eight waves takes a few row tiles of one matrix.  The waves
+// split the columns, in tiles of 128 dealt in turn (with fewer than eight
+// column tiles, they split the row tiles too); each streams its 1-KiB code
+// tiles through a ring of registers, loads for kDepth tiles ahead in flight,
+// the first of them issued before the rows of x are staged in LDS.  Partial
+// sums meet in LDS once, at the end, and are added in a fixed order.
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
+// LDS for x and for partial sums: together with the list of rows 80 KB, so
+// that two workgroups share a compute unit (128 KB for the 64-row form).  The
+// sums take 1 KB a row tile, half of a SwiGLU, wave along the columns and 16
+// rows of x.
+constexpr int kLds = (80 << 10) - 256, kLdsMany = 128 << 10;
+// Registers: the ring of scales of 32 columns for two halves, and the sums of
+// 64 rows, take more than the 128 that two workgroups a compute unit leave.
+constexpr bool roomy(int group, bool swiglu, int ct) { return ct > 1 || (swiglu && group == 32); }
 
 struct Q4 {
   const uint16_t* x;
@@ -38,7 +54,10 @@ struct Q4 {
   void* y;
   int64_t ldx, ldy;
   int n, k, rows, x_div, n_mats, out_type;
-  int tn, tk;               // tiles of a matrix
+  int tn, tk;               // tiles of a matrix; with SwiGLU tn counts the gate's
+  int split, split_log2;    // waves along the columns (a power of two)
+  int per_wg;               // row tiles of a workgroup
+  int x_bytes;              // LDS for x; the rest is for partial sums
 };
 
 template <bool BF>
@@ -50,30 +69,39 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // Codes 0 .. 7 of a word as 16 + c, in the order (0,4) (1,5) (2,6) (3,7).
+// `base` holds the exponent bits of 16.0 twice, in a register that the compiler
+// cannot see through: with two literals it would split each and-or in two.
+// (Written as inline assembly, the and-or escapes the compiler's count of the
+// cycles that a matrix instruction goes on reading its addend, and may
+// overwrite it: seen as wrong sums where two products share one addend.)
 template <bool BF>
-__device__ __forceinline__ u32x4 unpack8(uint32_t w) {
+__device__ __forceinline__ uint32_t opaque_base() {
+  uint32_t b = BF ? 0x41804180u : 0x4C004C00u;
+  asm("" : "+v"(b));
+  return b;
+}
+template <bool BF>
+__device__ __forceinline__ u32x4 unpack8(uint32_t w, uint32_t base) {
   constexpr int at = BF ? 3 : 6;                     // lowest of the top four mantissa bits
-  constexpr uint32_t mask = 0x000F000Fu << at, base = BF ? 0x41804180u : 0x4C004C00u;
-  u32x4 v;
-  v[0] = dev::andor(w << at, mask, base);
-  v[1] = BF ? dev::andor(w >> 1, mask, base) : dev::andor(w << 2, mask, base);
-  v[2] = dev::andor(w >> (8 - at), mask, base);
-  v[3] = dev::andor(w >> (12 - at), mask, base);
-  return v;
+  constexpr uint32_t mask = 0x000F000Fu << at;
+  return u32x4{((w << at) & mask) | base, ((BF ? w >> 1 : w << 2) & mask) | base, ((w >> (8 - at)) & mask) | base,
+               ((w >> (12 - at)) & mask) | base};
 }
 
-// Eight values of x in the same order, and their sum.
-template <bool BF>
-__device__ __forceinline__ u32x4 order8(u32x4 x, float& sum) {
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (BF) s += dev::bf16_bits_to_f32(x[i] & 0xFFFFu) + dev::bf16_bits_to_f32(x[i] >> 16);
-    else s += dev::h2_lo(x[i]) + dev::h2_hi(x[i]);
-  }
-  sum = s;
+// Eight values of x in the same order.
+__device__ __forceinline__ u32x4 order8(u32x4 x) {
   return u32x4{(x[0] & 0xFFFFu) | x[2] << 16, x[0] >> 16 | (x[2] & 0xFFFF0000u), (x[1] & 0xFFFFu) | x[3] << 16,
                x[1] >> 16 | (x[3] & 0xFFFF0000u)};
+}
+
+// -(16 + z) in every element: its product with x is what the codes' base and
+// zero add to the sum, exact in 16 bits for z = 0 .. 15.
+template <bool BF>
+__device__ __forceinline__ u32x4 offset8(uint32_t z) {
+  // bf16: 16 + z = 0x41800000 + z * 2^19 as fp32 bits; f16: 0x4C00 + z * 2^6
+  const uint32_t h = BF ? 0xC180u + (z << 3) : 0xCC00u + (z << 6);
+  const uint32_t w = h | h << 16;
+  return u32x4{w, w, w, w};
 }
 
 __device__ __forceinline__ void put(void* y, int64_t at, float v, int type) {
@@ -103,101 +131,218 @@ __device__ __forceinline__ int nth_row(uint64_t m, int c) {
   return m ? __ffsll(static_cast<unsigned long long>(m)) - 1 : -1;
 }
 
-template <bool BF, int G, bool Z, bool SW>
-__global__ __launch_bounds__(64 * kQ4Waves) void k_q4(Q4 a) {
+// CT: column tiles of 16 rows of x.  (Rows that chose one matrix: 16 at a
+// time.)
+template <bool BF, int G, bool Z, bool SW, int CT>
+__global__ __launch_bounds__(kThreads, roomy(G, SW, CT) ? 2 : 4) void k_q4(Q4 a) {
   constexpr int H = SW ? 2 : 1;
-  __shared__ f32x4 part[kQ4Waves][H][64];
+  constexpr int kPer = 128 / G;          // groups of a tile
+  constexpr int kDepth = CT > 1 ? (SW ? 1 : 2) : roomy(G, SW, CT) ? 4 : 4 / H;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ int member[CT * 16];        // the row of y in each column
   const int tid = threadIdx.x, lane = tid & 63, wave = dev::uniform(tid >> 6), col = lane & 15, q = lane >> 4;
+  const uint32_t unit = opaque_base<BF>();
   int mat;
-  uint64_t rows = rows_of(a, blockIdx.y, mat);
-  if (!rows) return;
+  const uint64_t all = rows_of(a, blockIdx.y, mat);
+  if (!all) return;
   const int out_n = SW ? a.n / 2 : a.n;
+  const int tile0 = blockIdx.x * a.per_wg, tiles = a.tn - tile0 < a.per_wg ? a.tn - tile0 : a.per_wg;
   if (mat < 0 || mat >= a.n_mats) {                 // no matrix: zeros for -1, else NaN
-    for (; rows; rows &= rows - 1) {
-      const int p = __ffsll(static_cast<unsigned long long>(rows)) - 1, c = blockIdx.x * 16 + tid;
-      if (tid < 16 && c < out_n) put(a.y, p * a.ldy + c, mat == -1 ? 0.0f : __builtin_nanf(""), a.out_type);
+    for (uint64_t m = all; m; m &= m - 1) {
+      const int p = __ffsll(static_cast<unsigned long long>(m)) - 1;
+      for (int i = tid; i < tiles * 16; i += kThreads)
+        if (tile0 * 16 + i < out_n) put(a.y, p * a.ldy + tile0 * 16 + i, mat == -1 ? 0.0f : __builtin_nanf(""), a.out_type);
     }
     return;
   }
-  const int64_t tiles = static_cast<int64_t>(a.tn) * a.tk;
-  constexpr int kPer = 128 / G;                     // groups of a tile
-  const u32x4* codes = reinterpret_cast<const u32x4*>(a.codes + mat * tiles * 1024);
-  const uint8_t* scales = a.scales + mat * tiles * kPer * 32;
-  const uint8_t* zeros = Z ? a.zeros + mat * tiles * kPer * 16 : nullptr;
-  for (; rows;) {
-    const int p = nth_row(rows, col);
-    const uint16_t* x = a.x + (p < 0 ? 0 : p / a.x_div) * a.ldx;
-    f32x4 out[H] = {};
-    for (int kt = wave; kt < a.tk; kt += kQ4Waves) {
-      u32x4 xv[4];
-      float sum[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = kt * 128 + j * 32 + q * 8;
-        u32x4 v{0, 0, 0, 0};
-        if (p >= 0 && k < a.k) __builtin_memcpy(&v, x + k, 16);
-        xv[j] = order8<BF>(v, sum[j]);
-        sum[j] += __shfl_xor(sum[j], 16, 64);
-        sum[j] += __shfl_xor(sum[j], 32, 64);
-      }
+  const int64_t mat_tiles = static_cast<int64_t>(a.tn) * H * a.tk;
+  const u32x4* codes = reinterpret_cast<const u32x4*>(a.codes + mat * mat_tiles * 1024) + lane;
+  const uint8_t* scales = a.scales + mat * mat_tiles * kPer * 32 + q * 8;
+  const uint8_t* zeros = Z ? a.zeros + mat * mat_tiles * kPer * 16 + col : nullptr;
+  const int ks = wave & (a.split - 1), lane_tile = wave >> a.split_log2, lanes_tile = kWaves >> a.split_log2;
+  MOE_Q4_LDS uint8_t* xl = (MOE_Q4_LDS uint8_t*)lds;
+  MOE_Q4_LDS float* part = (MOE_Q4_LDS float*)(lds + a.x_bytes);
+  // this wave's row tiles: lane_tile, lane_tile + lanes_tile, ...
+  const int mine = (tiles - lane_tile + lanes_tile - 1) / lanes_tile;
+
+  for (uint64_t rest = all; rest;) {
+  const uint64_t rows = rest;
+  const int left = __popcll(rows), count = left < CT * 16 ? left : CT * 16;
+  // x chunk (eight columns) c of column j lies at (c * held + j) * 16; lanes
+  // past the last column repeat one (their products belong to no row)
+  const int held = CT > 1 ? CT * 16 : count <= 1 ? 1 : count <= 2 ? 2 : count <= 4 ? 4 : count <= 8 ? 8 : 16;
+  const int span = a.x_bytes / (held * 256) >> a.split_log2 << a.split_log2;   // column tiles of x at a time
+  if (rest != all) __syncthreads();
+  if (tid < CT * 16) member[tid] = nth_row(rows, tid);
+  for (int i = 0; i < CT * 16; ++i) rest &= rest - 1;
+
+  for (int k0 = 0; k0 < a.tk; k0 += span) {
+    const int kn = a.tk - k0 < span ? a.tk - k0 : span;    // column tiles of this pass
+    const int each = (kn - ks + a.split - 1) >> a.split_log2;  // of which this wave's
+    const int items = mine > 0 && each > 0 ? mine * each : 0;
+
+    u32x4 w[kDepth][H];
+    f16x4 d[kDepth][H][kPer];
+    uint8_t z[kDepth][H][kPer];
+    int lt = 0, lk = 0;                                        // the next item to load
+    const auto load = [&](int s) {
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        const int64_t t = static_cast<int64_t>(blockIdx.x + h * (a.tn / 2)) * a.tk + kt;
-        const u32x4 w = codes[t * 64 + lane];
+        const int64_t t = static_cast<int64_t>(tile0 + lane_tile + lt * lanes_tile + h * a.tn) * a.tk + k0 + ks + lk * a.split;
+        w[s][h] = codes[t * 64];
 #pragma unroll
         for (int g = 0; g < kPer; ++g) {
-          float s = 0.0f;
+          d[s][h][g] = *reinterpret_cast<const f16x4*>(scales + (t * kPer + g) * 32);
+          if constexpr (Z) z[s][h][g] = zeros[(t * kPer + g) * 16];
+        }
+      }
+      // past the last item the loads repeat it: without a branch around them
+      // the compiler knows how many are in flight and waits for the oldest only
+      const bool wrap = lk + 1 == each, last = wrap && lt + 1 == mine;
+      lt += wrap && !last ? 1 : 0;
+      lk = last ? lk : wrap ? 0 : lk + 1;
+    };
+    if (items) {
 #pragma unroll
-          for (int j = 0; j < G / 32; ++j) s += sum[g * (G / 32) + j];
-          uint32_t z4 = 0x08080808u;
-          if constexpr (Z) z4 = *reinterpret_cast<const uint32_t*>(zeros + (t * kPer + g) * 16 + q * 4);
-          const f16x4 d = *reinterpret_cast<const f16x4*>(scales + (t * kPer + g) * 32 + q * 8);
-          f32x4 acc;
+      for (int s = 0; s < kDepth; ++s) load(s);
+    }
+
+    __syncthreads();                                           // x of the last pass is used, member is there
+    for (int c = tid; c < kn * 16 * held; c += kThreads) {
+      const int chunk = c / held, j = c - chunk * held, k = (k0 * 16 + chunk) * 8;
+      const int p = member[j];
+      if (p < 0) continue;
+      u32x4 v{0, 0, 0, 0};
+      if (k < a.k) __builtin_memcpy(&v, a.x + (p / a.x_div) * a.ldx + k, 16);
+      *reinterpret_cast<MOE_Q4_LDS u32x4*>(xl + c * 16) = order8(v);
+    }
+    __syncthreads();
+
+    f32x4 out[H][CT] = {};
+    int ct = 0, ck = 0;                                        // the item being multiplied
+    const MOE_Q4_LDS uint8_t* xq = xl + (q * held + (CT > 1 ? col : col & (held - 1))) * 16;
+    for (int base = 0; base < items; base += kDepth) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = -static_cast<float>(16 + (z4 >> (8 * i) & 255u)) * s;
+      for (int s = 0; s < kDepth; ++s) {
+        if (base + s >= items) break;
+        const MOE_Q4_LDS uint8_t* xt = xq + (ks + ck * a.split) * 16 * held * 16;
+        f32x4 acc[H][CT];
 #pragma unroll
-          for (int j = 0; j < G / 32; ++j) acc = mma<BF>(unpack8<BF>(w[g * (G / 32) + j]), xv[g * (G / 32) + j], acc);
+        for (int j = 0; j < 4; ++j) {
+          const int g = j * 32 / G;
+          const bool first = j * 32 % G == 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) out[h][i] += static_cast<float>(d[i]) * acc[i];
+          for (int c = 0; c < CT; ++c) {
+            const u32x4 xv = *reinterpret_cast<const MOE_Q4_LDS u32x4*>(xt + (j * 4 * held + c * 16) * 16);
+            f32x4 start{0, 0, 0, 0};
+            if constexpr (!Z) start = mma<BF>(offset8<BF>(8), xv, start);   // one for both halves
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              f32x4 sum = first ? f32x4{0, 0, 0, 0} : acc[h][c];
+              if constexpr (Z) sum = mma<BF>(offset8<BF>(z[s][h][g]), xv, sum);
+              else if (first) sum = start;
+              else sum += start;
+              acc[h][c] = mma<BF>(unpack8<BF>(w[s][h][j], unit), xv, sum);
+              if (j * 32 % G == G - 32) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[h][c][i] += static_cast<float>(d[s][h][g][i]) * acc[h][c][i];
+              }
+            }
+          }
+        }
+        load(s);
+        if (++ck == each) {
+          // the tile's columns are done: this wave's share of its sums
+          ck = 0;
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+              if (CT > 1 || col < held) {
+                MOE_Q4_LDS f32x4* at = reinterpret_cast<MOE_Q4_LDS f32x4*>(part) +
+                    ((((lane_tile + ct * lanes_tile) * H + h) << a.split_log2 | ks) * 4 + q) * held + c * 16 + (CT > 1 ? col : col & (held - 1));
+                *at = k0 ? *at + out[h][c] : out[h][c];
+              }
+              out[h][c] = f32x4{0, 0, 0, 0};
+            }
+          ++ct;
         }
       }
     }
+    // waves without a column tile in the first pass add nothing
+    if (k0 == 0 && each <= 0)
+      for (int t = 0; t < mine; ++t)
 #pragma unroll
-    for (int h = 0; h < H; ++h) part[wave][h][lane] = out[h];
-    __syncthreads();
-    if (wave == 0 && p >= 0) {
-      f32x4 v[H] = {};
+        for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int h = 0; h < H; ++h)
+          for (int c = 0; c < CT; ++c)
+            if (CT > 1 || col < held)
+              reinterpret_cast<MOE_Q4_LDS f32x4*>(part)[((((lane_tile + t * lanes_tile) * H + h) << a.split_log2 | ks) * 4 + q) * held +
+                                                        c * 16 + (CT > 1 ? col : col & (held - 1))] = f32x4{0, 0, 0, 0};
+  }
+  __syncthreads();
+
+  // one thread per output: row n of a tile, column j
+  for (int i = tid; i < tiles * 16 * held; i += kThreads) {
+    const int r = i & 15, j = (i >> 4) % held, t = (i >> 4) / held;
+    if (j >= count) continue;
+    float v[H];
 #pragma unroll
-        for (int w = 0; w < kQ4Waves; ++w) v[h] += part[w][h][lane];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = blockIdx.x * 16 + q * 4 + i;
-        float o = v[0][i];
-        if constexpr (SW) o = o / (1.0f + __expf(-o)) * v[1][i];
-        if (c < out_n) put(a.y, p * a.ldy + c, o, a.out_type);
-      }
+    for (int h = 0; h < H; ++h) {
+      v[h] = 0.0f;
+      for (int s = 0; s < a.split; ++s)
+        v[h] += part[(((((t * H + h) << a.split_log2) | s) * 4 + (r >> 2)) * held + j) * 4 + (r & 3)];
     }
-    __syncthreads();
-    for (int i = 0; i < 16; ++i) rows &= rows - 1;
+    float o = v[0];
+    if constexpr (SW) o = o / (1.0f + __expf(-o)) * v[1];
+    const int c = (tile0 + t) * 16 + r, p = member[j];
+    if (c < out_n) put(a.y, p * a.ldy + c, o, a.out_type);
+  }
   }
 }
 
 namespace {
 
-template <bool BF, int G, bool Z>
-void go(const Q4& a, bool swiglu, hipStream_t s) {
-  const dim3 block(64 * kQ4Waves);
-  const uint32_t y = a.idx ? a.rows : 1;
-  if (swiglu) hipLaunchKernelGGL((k_q4<BF, G, Z, true>), dim3(a.tn / 2, y), block, 0, s, a);
-  else hipLaunchKernelGGL((k_q4<BF, G, Z, false>), dim3(a.tn, y), block, 0, s, a);
+template <bool BF, int G, bool Z, bool SW>
+void go(Q4 a, hipStream_t s) {
+  constexpr int H = SW ? 2 : 1;
+  if (SW) a.tn /= 2;
+  // rows of one matrix: 16 columns of the instruction, or four times 16
+  const bool many = !a.idx && a.rows > 16;
+  int held = many ? 64 : 1;
+  while (held < 16 && held < a.rows) held *= 2;
+  // x takes held * 256 bytes a column tile.  Dense: room for all of it up to
+  // 63 KB; with a matrix per row few rows share one, and its sums count more.
+  const int lds = many ? kLdsMany : kLds;
+  a.x_bytes = many ? 64 << 10 : a.idx ? 32 << 10 : 63 << 10;
+  const int tiles_held = a.x_bytes / (held * 256);   // >= 4
+  // the waves split the columns, as far as there are column tiles and as a
+  // column tile each fits
+  a.split_log2 = a.tk >= 8 && tiles_held >= 8 ? 3 : a.tk >= 4 ? 2 : a.tk >= 2 ? 1 : 0;
+  a.split = 1 << a.split_log2;
+  // row tiles of a workgroup: enough to spread the staging of x over them,
+  // as long as every compute unit has two workgroups, and as the sums fit
+  const int64_t mats = a.idx ? (a.rows < a.n_mats ? a.rows : a.n_mats) : 1;
+  const int fit = (lds - a.x_bytes) / (held * 64 * H * a.split);   // >= 1
+  int64_t per = mats * a.tn / 1024;
+  if (per < kWaves / a.split) per = kWaves / a.split;
+  if (per > 8) per = 8;
+  if (per > fit) per = fit;
+  a.per_wg = static_cast<int>(per);
+  const dim3 grid((a.tn + a.per_wg - 1) / a.per_wg, a.idx ? a.rows : 1);
+  if (many) hipLaunchKernelGGL((k_q4<BF, G, Z, SW, 4>), grid, dim3(kThreads), lds, s, a);
+  else hipLaunchKernelGGL((k_q4<BF, G, Z, SW, 1>), grid, dim3(kThreads), lds, s, a);
 }
 
 template <bool BF, int G>
 void go(const Q4& a, bool swiglu, hipStream_t s) {
-  if (a.zeros) go<BF, G, true>(a, swiglu, s);
-  else go<BF, G, false>(a, swiglu, s);
+  if (a.zeros) {
+    if (swiglu) go<BF, G, true, true>(a, s);
+    else go<BF, G, true, false>(a, s);
+  } else {
+    if (swiglu) go<BF, G, false, true>(a, s);
+    else go<BF, G, false, false>(a, s);
+  }
 }
 
 template <bool BF>
