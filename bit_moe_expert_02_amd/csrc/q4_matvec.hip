@@ -25,26 +25,23 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+using dev::u32x2;
 using dev::u32x4;
 #define MOE_Q4_LDS __attribute__((address_space(3)))
 
 // A workgroup of eight waves takes a few row tiles of one matrix.  The waves
 // split the columns, in tiles of 128 dealt in turn (with fewer than eight
-// column tiles, they split the row tiles too); each streams its 1-KiB code
-// tiles through a ring of registers, loads for kDepth tiles ahead in flight,
+// column tiles, they split the row tiles too).  For a column tile a wave reads
+// its piece of x from LDS once and multiplies T row tiles by it; loads for T
+// row tiles times D column tiles ahead are in flight in a ring of registers,
 // the first of them issued before the rows of x are staged in LDS.  Partial
 // sums meet in LDS once, at the end, and are added in a fixed order.
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 // LDS for x and for partial sums: together with the list of rows 80 KB, so
 // that two workgroups share a compute unit (128 KB for the 64-row form).  The
-// sums take 1 KB a row tile, half of a SwiGLU, wave along the columns and 16
-// rows of x.
+// sums take 64 bytes a row of x, row tile, half of a SwiGLU and wave.
 constexpr int kLds = (80 << 10) - 256, kLdsMany = 128 << 10;
-// Registers: the ring of scales of 32 columns for two halves, and the sums of
-// 64 rows, take more than the 128 that two workgroups a compute unit leave.
-constexpr bool roomy(int group, bool swiglu, int ct) { return ct > 1 || (swiglu && group == 32); }
-
 struct Q4 {
   const uint16_t* x;
   const int32_t* idx;
@@ -56,7 +53,6 @@ struct Q4 {
   int n, k, rows, x_div, n_mats, out_type;
   int tn, tk;               // tiles of a matrix; with SwiGLU tn counts the gate's
   int split, split_log2;    // waves along the columns (a power of two)
-  int per_wg;               // row tiles of a workgroup
   int x_bytes;              // LDS for x; the rest is for partial sums
 };
 
@@ -104,6 +100,18 @@ __device__ __forceinline__ u32x4 offset8(uint32_t z) {
   return u32x4{w, w, w, w};
 }
 
+// The value that lane g (0 .. 3) of each row of 16 lanes holds, in all of them.
+__device__ __forceinline__ f16x4 lane_of_row(u32x2 v, int g) {
+  u32x2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r[i] = g == 0   ? __builtin_amdgcn_mov_dpp(v[i], 0x150, 0xF, 0xF, true)
+           : g == 1 ? __builtin_amdgcn_mov_dpp(v[i], 0x151, 0xF, 0xF, true)
+           : g == 2 ? __builtin_amdgcn_mov_dpp(v[i], 0x152, 0xF, 0xF, true)
+                    : __builtin_amdgcn_mov_dpp(v[i], 0x153, 0xF, 0xF, true);
+  return __builtin_bit_cast(f16x4, r);
+}
+
 __device__ __forceinline__ void put(void* y, int64_t at, float v, int type) {
   if (type == MOE_T_F32) static_cast<float*>(y)[at] = v;
   else if (type == MOE_T_BF16) static_cast<uint16_t*>(y)[at] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
@@ -132,12 +140,11 @@ __device__ __forceinline__ int nth_row(uint64_t m, int c) {
 }
 
 // CT: column tiles of 16 rows of x.  (Rows that chose one matrix: 16 at a
-// time.)
-template <bool BF, int G, bool Z, bool SW, int CT>
-__global__ __launch_bounds__(kThreads, roomy(G, SW, CT) ? 2 : 4) void k_q4(Q4 a) {
+// time.)  T row tiles a wave, D column tiles ahead.
+template <bool BF, int G, bool Z, bool SW, int CT, int T, int D>
+__global__ __launch_bounds__(kThreads, CT > 1 ? 2 : 4) void k_q4(Q4 a) {
   constexpr int H = SW ? 2 : 1;
   constexpr int kPer = 128 / G;          // groups of a tile
-  constexpr int kDepth = CT > 1 ? (SW ? 1 : 2) : roomy(G, SW, CT) ? 4 : 4 / H;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int member[CT * 16];        // the row of y in each column
   const int tid = threadIdx.x, lane = tid & 63, wave = dev::uniform(tid >> 6), col = lane & 15, q = lane >> 4;
@@ -146,7 +153,8 @@ __global__ __launch_bounds__(kThreads, roomy(G, SW, CT) ? 2 : 4) void k_q4(Q4 a)
   const uint64_t all = rows_of(a, blockIdx.y, mat);
   if (!all) return;
   const int out_n = SW ? a.n / 2 : a.n;
-  const int tile0 = blockIdx.x * a.per_wg, tiles = a.tn - tile0 < a.per_wg ? a.tn - tile0 : a.per_wg;
+  const int per_wg = T * kWaves >> a.split_log2;
+  const int tile0 = blockIdx.x * per_wg, tiles = a.tn - tile0 < per_wg ? a.tn - tile0 : per_wg;
   if (mat < 0 || mat >= a.n_mats) {                 // no matrix: zeros for -1, else NaN
     for (uint64_t m = all; m; m &= m - 1) {
       const int p = __ffsll(static_cast<unsigned long long>(m)) - 1;
@@ -157,151 +165,172 @@ __global__ __launch_bounds__(kThreads, roomy(G, SW, CT) ? 2 : 4) void k_q4(Q4 a)
   }
   const int64_t mat_tiles = static_cast<int64_t>(a.tn) * H * a.tk;
   const u32x4* codes = reinterpret_cast<const u32x4*>(a.codes + mat * mat_tiles * 1024) + lane;
-  const uint8_t* scales = a.scales + mat * mat_tiles * kPer * 32 + q * 8;
+  // lane g of a row of 16 lanes loads the scales of group g for the row's four outputs
+  const uint8_t* scales = a.scales + mat * mat_tiles * kPer * 32 + (col & (kPer - 1)) * 32 + q * 8;
   const uint8_t* zeros = Z ? a.zeros + mat * mat_tiles * kPer * 16 + col : nullptr;
-  const int ks = wave & (a.split - 1), lane_tile = wave >> a.split_log2, lanes_tile = kWaves >> a.split_log2;
+  const int ks = wave & (a.split - 1), first_tile = (wave >> a.split_log2) * T;
   MOE_Q4_LDS uint8_t* xl = (MOE_Q4_LDS uint8_t*)lds;
-  MOE_Q4_LDS float* part = (MOE_Q4_LDS float*)(lds + a.x_bytes);
-  // this wave's row tiles: lane_tile, lane_tile + lanes_tile, ...
-  const int mine = (tiles - lane_tile + lanes_tile - 1) / lanes_tile;
+  MOE_Q4_LDS f32x4* part = (MOE_Q4_LDS f32x4*)(lds + a.x_bytes);
 
   for (uint64_t rest = all; rest;) {
-  const uint64_t rows = rest;
-  const int left = __popcll(rows), count = left < CT * 16 ? left : CT * 16;
-  // x chunk (eight columns) c of column j lies at (c * held + j) * 16; lanes
-  // past the last column repeat one (their products belong to no row)
-  const int held = CT > 1 ? CT * 16 : count <= 1 ? 1 : count <= 2 ? 2 : count <= 4 ? 4 : count <= 8 ? 8 : 16;
-  const int span = a.x_bytes / (held * 256) >> a.split_log2 << a.split_log2;   // column tiles of x at a time
-  if (rest != all) __syncthreads();
-  if (tid < CT * 16) member[tid] = nth_row(rows, tid);
-  for (int i = 0; i < CT * 16; ++i) rest &= rest - 1;
+    const uint64_t rows = rest;
+    const int left = __popcll(rows), count = left < CT * 16 ? left : CT * 16;
+    // x chunk (eight columns) c of column j lies at (c * held + j) * 16; lanes
+    // past the last column repeat one (their products belong to no row)
+    const int log_held = CT > 1 ? 6 : count <= 1 ? 0 : count <= 2 ? 1 : count <= 4 ? 2 : count <= 8 ? 3 : 4, held = 1 << log_held;
+    const int span = a.x_bytes >> (log_held + 8) >> a.split_log2 << a.split_log2;   // column tiles of x at a time
+    if (rest != all) __syncthreads();
+    if (tid < CT * 16) member[tid] = nth_row(rows, tid);
+    for (int i = 0; i < CT * 16; ++i) rest &= rest - 1;
 
-  for (int k0 = 0; k0 < a.tk; k0 += span) {
-    const int kn = a.tk - k0 < span ? a.tk - k0 : span;    // column tiles of this pass
-    const int each = (kn - ks + a.split - 1) >> a.split_log2;  // of which this wave's
-    const int items = mine > 0 && each > 0 ? mine * each : 0;
+    f32x4 out[T][H][CT] = {};
+    for (int k0 = 0; k0 < a.tk; k0 += span) {
+      const int kn = a.tk - k0 < span ? a.tk - k0 : span;        // column tiles of this pass
+      const int each = (kn - ks + a.split - 1) >> a.split_log2;  // of which this wave's
 
-    u32x4 w[kDepth][H];
-    f16x4 d[kDepth][H][kPer];
-    uint8_t z[kDepth][H][kPer];
-    int lt = 0, lk = 0;                                        // the next item to load
-    const auto load = [&](int s) {
+      u32x4 w[D][T][H];
+      u32x2 d[D][T][H];
+      uint8_t z[D][T][H][kPer];
+      // Column tile `i` of this wave's; past the last the loads repeat it, as
+      // row tiles past the matrix repeat its last: without a branch around
+      // them the compiler knows how many are in flight and waits for the
+      // oldest only.
+      const auto load = [&](int s, int t, int i) {
+        const int kt = k0 + ks + (i < each ? i : each - 1) * a.split;
+        const int row = tile0 + first_tile + t;
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const int64_t t = static_cast<int64_t>(tile0 + lane_tile + lt * lanes_tile + h * a.tn) * a.tk + k0 + ks + lk * a.split;
-        w[s][h] = codes[t * 64];
+        for (int h = 0; h < H; ++h) {
+          const int64_t at = static_cast<int64_t>((row < a.tn ? row : a.tn - 1) + h * a.tn) * a.tk + kt;
+          w[s][t][h] = codes[at * 64];
+          d[s][t][h] = *reinterpret_cast<const u32x2*>(scales + at * kPer * 32);
+          if constexpr (Z)
 #pragma unroll
-        for (int g = 0; g < kPer; ++g) {
-          d[s][h][g] = *reinterpret_cast<const f16x4*>(scales + (t * kPer + g) * 32);
-          if constexpr (Z) z[s][h][g] = zeros[(t * kPer + g) * 16];
+            for (int g = 0; g < kPer; ++g) z[s][t][h][g] = zeros[(at * kPer + g) * 16];
         }
+      };
+      if (each > 0) {
+#pragma unroll
+        for (int s = 0; s < D; ++s)
+#pragma unroll
+          for (int t = 0; t < T; ++t) load(s, t, s);
       }
-      // past the last item the loads repeat it: without a branch around them
-      // the compiler knows how many are in flight and waits for the oldest only
-      const bool wrap = lk + 1 == each, last = wrap && lt + 1 == mine;
-      lt += wrap && !last ? 1 : 0;
-      lk = last ? lk : wrap ? 0 : lk + 1;
-    };
-    if (items) {
-#pragma unroll
-      for (int s = 0; s < kDepth; ++s) load(s);
-    }
 
-    __syncthreads();                                           // x of the last pass is used, member is there
-    for (int c = tid; c < kn * 16 * held; c += kThreads) {
-      const int chunk = c / held, j = c - chunk * held, k = (k0 * 16 + chunk) * 8;
-      const int p = member[j];
-      if (p < 0) continue;
-      u32x4 v{0, 0, 0, 0};
-      if (k < a.k) __builtin_memcpy(&v, a.x + (p / a.x_div) * a.ldx + k, 16);
-      *reinterpret_cast<MOE_Q4_LDS u32x4*>(xl + c * 16) = order8(v);
-    }
-    __syncthreads();
+      __syncthreads();                                           // x of the last pass is used, member is there
+      for (int c = tid; c < kn * 16 << log_held; c += kThreads) {
+        const int k = (k0 * 16 + (c >> log_held)) * 8, p = member[c & (held - 1)];
+        if (p < 0) continue;
+        u32x4 v{0, 0, 0, 0};
+        if (k < a.k) __builtin_memcpy(&v, a.x + (a.x_div == 1 ? p : p / a.x_div) * a.ldx + k, 16);
+        *reinterpret_cast<MOE_Q4_LDS u32x4*>(xl + c * 16) = order8(v);
+      }
+      __syncthreads();
 
-    f32x4 out[H][CT] = {};
-    int ct = 0, ck = 0;                                        // the item being multiplied
-    const MOE_Q4_LDS uint8_t* xq = xl + (q * held + (CT > 1 ? col : col & (held - 1))) * 16;
-    for (int base = 0; base < items; base += kDepth) {
+      const MOE_Q4_LDS uint8_t* xq = xl + ((q << log_held) + (CT > 1 ? col : col & (held - 1))) * 16;
+      for (int i0 = 0; i0 < each; i0 += D) {
 #pragma unroll
-      for (int s = 0; s < kDepth; ++s) {
-        if (base + s >= items) break;
-        const MOE_Q4_LDS uint8_t* xt = xq + (ks + ck * a.split) * 16 * held * 16;
-        f32x4 acc[H][CT];
+        for (int s = 0; s < D; ++s) {
+          if (i0 + s >= each) break;
+          const MOE_Q4_LDS uint8_t* xt = xq + ((ks + (i0 + s) * a.split) * 256 << log_held);
+          u32x4 xv[4][CT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int g = j * 32 / G;
-          const bool first = j * 32 % G == 0;
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const u32x4 xv = *reinterpret_cast<const MOE_Q4_LDS u32x4*>(xt + (j * 4 * held + c * 16) * 16);
-            f32x4 start{0, 0, 0, 0};
-            if constexpr (!Z) start = mma<BF>(offset8<BF>(8), xv, start);   // one for both halves
+            for (int c = 0; c < CT; ++c)
+              xv[j][c] = *reinterpret_cast<const MOE_Q4_LDS u32x4*>(xt + ((j * 64 << log_held) + c * 256));
+          // symmetric: what base and zero add is the same for every row tile
+          f32x4 start[kPer][CT];
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-              f32x4 sum = first ? f32x4{0, 0, 0, 0} : acc[h][c];
-              if constexpr (Z) sum = mma<BF>(offset8<BF>(z[s][h][g]), xv, sum);
-              else if (first) sum = start;
-              else sum += start;
-              acc[h][c] = mma<BF>(unpack8<BF>(w[s][h][j], unit), xv, sum);
-              if (j * 32 % G == G - 32) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[h][c][i] += static_cast<float>(d[s][h][g][i]) * acc[h][c][i];
-              }
-            }
-          }
-        }
-        load(s);
-        if (++ck == each) {
-          // the tile's columns are done: this wave's share of its sums
-          ck = 0;
-#pragma unroll
-          for (int h = 0; h < H; ++h)
+          for (int g = 0; g < kPer; ++g)
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
-              if (CT > 1 || col < held) {
-                MOE_Q4_LDS f32x4* at = reinterpret_cast<MOE_Q4_LDS f32x4*>(part) +
-                    ((((lane_tile + ct * lanes_tile) * H + h) << a.split_log2 | ks) * 4 + q) * held + c * 16 + (CT > 1 ? col : col & (held - 1));
-                *at = k0 ? *at + out[h][c] : out[h][c];
-              }
-              out[h][c] = f32x4{0, 0, 0, 0};
+              start[g][c] = f32x4{0, 0, 0, 0};
+              if constexpr (!Z)
+#pragma unroll
+                for (int j = 0; j < G / 32; ++j) start[g][c] = mma<BF>(offset8<BF>(8), xv[g * (G / 32) + j][c], start[g][c]);
             }
-          ++ct;
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+#pragma unroll
+              for (int g = 0; g < kPer; ++g) {
+                f32x4 acc[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) acc[c] = start[g][c];
+#pragma unroll
+                for (int j = 0; j < G / 32; ++j) {
+                  const u32x4 code = unpack8<BF>(w[s][t][h][g * (G / 32) + j], unit);
+#pragma unroll
+                  for (int c = 0; c < CT; ++c) {
+                    if constexpr (Z) acc[c] = mma<BF>(offset8<BF>(z[s][t][h][g]), xv[g * (G / 32) + j][c], acc[c]);
+                    acc[c] = mma<BF>(code, xv[g * (G / 32) + j][c], acc[c]);
+                  }
+                }
+                const f16x4 scale = lane_of_row(d[s][t][h], g);
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) out[t][h][c][i] += static_cast<float>(scale[i]) * acc[c][i];
+              }
+            }
+            load(s, t, i0 + s + D);
+          }
         }
       }
     }
-    // waves without a column tile in the first pass add nothing
-    if (k0 == 0 && each <= 0)
-      for (int t = 0; t < mine; ++t)
+    // [row tile][half][wave along the columns][quarter][column]
+    if (CT > 1 || col < held) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int c = 0; c < CT; ++c)
-            if (CT > 1 || col < held)
-              reinterpret_cast<MOE_Q4_LDS f32x4*>(part)[((((lane_tile + t * lanes_tile) * H + h) << a.split_log2 | ks) * 4 + q) * held +
-                                                        c * 16 + (CT > 1 ? col : col & (held - 1))] = f32x4{0, 0, 0, 0};
-  }
-  __syncthreads();
-
-  // one thread per output: row n of a tile, column j
-  for (int i = tid; i < tiles * 16 * held; i += kThreads) {
-    const int r = i & 15, j = (i >> 4) % held, t = (i >> 4) / held;
-    if (j >= count) continue;
-    float v[H];
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      v[h] = 0.0f;
-      for (int s = 0; s < a.split; ++s)
-        v[h] += part[(((((t * H + h) << a.split_log2) | s) * 4 + (r >> 2)) * held + j) * 4 + (r & 3)];
+            part[((((((first_tile + t) * H + h) << a.split_log2) | ks) * 4 + q) << log_held) + c * 16 + col] = out[t][h][c];
     }
-    float o = v[0];
-    if constexpr (SW) o = o / (1.0f + __expf(-o)) * v[1];
-    const int c = (tile0 + t) * 16 + r, p = member[j];
-    if (c < out_n) put(a.y, p * a.ldy + c, o, a.out_type);
-  }
+    __syncthreads();
+
+    // one thread per output: row r of a tile, column j
+    const MOE_Q4_LDS float* sums = reinterpret_cast<const MOE_Q4_LDS float*>(part);
+    for (int i = tid; i < tiles * 16 << log_held; i += kThreads) {
+      const int r = i & 15, j = (i >> 4) & (held - 1), t = i >> (4 + log_held);
+      if (j >= count) continue;
+      float v[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        v[h] = 0.0f;
+        for (int s = 0; s < a.split; ++s)
+          v[h] += sums[((((((t * H + h) << a.split_log2) | s) * 4 + (r >> 2)) << log_held) + j) * 4 + (r & 3)];
+      }
+      float o = v[0];
+      if constexpr (SW) o = o / (1.0f + __expf(-o)) * v[1];
+      const int c = (tile0 + t) * 16 + r, p = member[j];
+      if (c < out_n) put(a.y, p * a.ldy + c, o, a.out_type);
+    }
   }
 }
 
 namespace {
+
+// Waves along the columns: as many as there are column tiles, and as a column
+// tile each of x fits in LDS (`held` rows take held * 256 bytes).
+int split_of(int tk, int held, int x_bytes) {
+  const int fit = x_bytes / (held * 256);
+  return tk >= 8 && fit >= 8 ? 3 : tk >= 4 && fit >= 4 ? 2 : tk >= 2 && fit >= 2 ? 1 : 0;
+}
+
+template <bool BF, int G, bool Z, bool SW, int CT, int T, int D>
+void run(Q4 a, int held, int lds, hipStream_t s) {
+  constexpr int H = SW ? 2 : 1;
+  a.split_log2 = split_of(a.tk, held, a.x_bytes);
+  a.split = 1 << a.split_log2;
+  const int per_wg = T * kWaves >> a.split_log2;
+  // the sums of the workgroup: always kWaves * T * H KB at most for 16 rows
+  static_assert(CT * kWaves * T * H <= 64, "the partial sums fit");
+  (void)H;
+  const dim3 grid((a.tn + per_wg - 1) / per_wg, a.idx ? a.rows : 1);
+  hipLaunchKernelGGL((k_q4<BF, G, Z, SW, CT, T, D>), grid, dim3(kThreads), lds, s, a);
+}
 
 template <bool BF, int G, bool Z, bool SW>
 void go(Q4 a, hipStream_t s) {
@@ -311,27 +340,23 @@ void go(Q4 a, hipStream_t s) {
   const bool many = !a.idx && a.rows > 16;
   int held = many ? 64 : 1;
   while (held < 16 && held < a.rows) held *= 2;
-  // x takes held * 256 bytes a column tile.  Dense: room for all of it up to
-  // 63 KB; with a matrix per row few rows share one, and its sums count more.
-  const int lds = many ? kLdsMany : kLds;
-  a.x_bytes = many ? 64 << 10 : a.idx ? 32 << 10 : 63 << 10;
-  const int tiles_held = a.x_bytes / (held * 256);   // >= 4
-  // the waves split the columns, as far as there are column tiles and as a
-  // column tile each fits
-  a.split_log2 = a.tk >= 8 && tiles_held >= 8 ? 3 : a.tk >= 4 ? 2 : a.tk >= 2 ? 1 : 0;
-  a.split = 1 << a.split_log2;
-  // row tiles of a workgroup: enough to spread the staging of x over them,
-  // as long as every compute unit has two workgroups, and as the sums fit
+  if (many) {
+    a.x_bytes = 64 << 10;
+    run<BF, G, Z, SW, 4, 1, 1>(a, held, kLdsMany, s);
+    return;
+  }
+  // several row tiles a wave as long as every compute unit has two workgroups
+  constexpr int T = 4 / H;
   const int64_t mats = a.idx ? (a.rows < a.n_mats ? a.rows : a.n_mats) : 1;
-  const int fit = (lds - a.x_bytes) / (held * 64 * H * a.split);   // >= 1
-  int64_t per = mats * a.tn / 1024;
-  if (per < kWaves / a.split) per = kWaves / a.split;
-  if (per > 8) per = 8;
-  if (per > fit) per = fit;
-  a.per_wg = static_cast<int>(per);
-  const dim3 grid((a.tn + a.per_wg - 1) / a.per_wg, a.idx ? a.rows : 1);
-  if (many) hipLaunchKernelGGL((k_q4<BF, G, Z, SW, 4>), grid, dim3(kThreads), lds, s, a);
-  else hipLaunchKernelGGL((k_q4<BF, G, Z, SW, 1>), grid, dim3(kThreads), lds, s, a);
+  const int sums = kWaves * H * held * 64;        // bytes, times the row tiles of a wave
+  a.x_bytes = (kLds - T * sums) & ~255;
+  const int waves_tile = kWaves >> split_of(a.tk, held, a.x_bytes);
+  if (mats * a.tn >= 512 * T * waves_tile) {
+    run<BF, G, Z, SW, 1, T, 1>(a, held, kLds, s);
+  } else {
+    a.x_bytes = (kLds - sums) & ~255;
+    run<BF, G, Z, SW, 1, 1, Z && SW && G == 32 ? 1 : T>(a, held, kLds, s);   // (registers)
+  }
 }
 
 template <bool BF, int G>
