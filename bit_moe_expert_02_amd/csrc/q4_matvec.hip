@@ -342,7 +342,7 @@ void go(Q4 a, hipStream_t s) {
   while (held < 16 && held < a.rows) held *= 2;
   if (many) {
     a.x_bytes = 64 << 10;
-    run<BF, G, Z, SW, 4, 1, 1>(a, held, kLdsMany, s);
+    run<BF, G, Z, SW, 4, 2 / H, 1>(a, held, kLdsMany, s);
     return;
   }
   // several row tiles a wave as long as every compute unit has two workgroups
