@@ -24,13 +24,17 @@ using dev::u32x4;
 // their count to the wave's counter of that id.  A scan over the waves and
 // the earlier workgroups' counts turns ranks into places.  Up to kPlanChunk
 // pairs one workgroup does it all; past that, k_plan_count leaves each chunk's
-// counts in the workspace, k_plan_scan sums them along the chunks, and
-// k_plan_place repeats the ranking with the sums as bases.
+// counts in the workspace and k_plan_place repeats the ranking with the sums of
+// the earlier chunks' as bases.  Each workgroup adds those up itself as long
+// as that is less reading than a launch takes time (kSumChunks); past it
+// k_plan_scan sums along the chunks in between.  196,608 pairs of 384 ids (96
+// chunks): 13.1 us with the scan's launch, 12.7 without.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kRounds = kPlanChunk / kPlanThreads;
 constexpr int kNone = 2047;   // past every group id: 11 bits
+constexpr int kSumChunks = 256;
 
 struct Plan {
   const int32_t* idx;
@@ -180,16 +184,30 @@ __global__ __launch_bounds__(64) void k_plan_scan(Plan a) {
   if (lane == 0) a.ws[static_cast<int64_t>(a.chunks) * a.groups + e] = base;
 }
 
+template <bool SCANNED>
 __global__ __launch_bounds__(kPlanThreads) void k_plan_place(Plan a) {
   int id[kRounds], rank[kRounds];
+  const int chunk = blockIdx.x, e = threadIdx.x;
+  // this thread's id: its pairs in earlier chunks and in all
+  int before = 0, total = 0;
+  if (e < a.groups) {
+    if constexpr (SCANNED) {
+      before = a.ws[static_cast<int64_t>(chunk) * a.groups + e];
+      total = a.ws[static_cast<int64_t>(a.chunks) * a.groups + e];
+    } else {
+#pragma unroll 32
+      for (int c = 0; c < a.chunks; ++c) {
+        const int v = a.ws[c * a.groups + e];
+        before += c < chunk ? v : 0;
+        total += v;
+      }
+    }
+  }
   clear_counts(a);
-  rank_pairs(a, blockIdx.x, id, rank, plan_lds + (threadIdx.x >> 6) * a.groups);
+  rank_pairs(a, chunk, id, rank, plan_lds + (threadIdx.x >> 6) * a.groups);
   __syncthreads();
-  const int32_t* mine = a.ws + static_cast<int64_t>(blockIdx.x) * a.groups;
-  const int32_t* totals = a.ws + static_cast<int64_t>(a.chunks) * a.groups;
   place_pairs(
-      a, blockIdx.x, id, rank, plan_lds, plan_lds + kPlanWaves * a.groups, [&](int e) { return totals[e]; },
-      [&](int e) { return mine[e]; });
+      a, chunk, id, rank, plan_lds, plan_lds + kPlanWaves * a.groups, [&](int) { return total; }, [&](int) { return before; });
 }
 
 // ---------------------------------------------------------------------------
@@ -437,8 +455,12 @@ int moe_group_plan(const int32_t* idx, int32_t rows, int32_t top_k, int32_t n_gr
     hipLaunchKernelGGL(k_plan_small, dim3(1), dim3(kPlanThreads), lds, s, a);
   } else {
     hipLaunchKernelGGL(k_plan_count, dim3(a.chunks), dim3(kPlanThreads), lds, s, a);
-    hipLaunchKernelGGL(k_plan_scan, dim3(n_groups), dim3(64), 0, s, a);
-    hipLaunchKernelGGL(k_plan_place, dim3(a.chunks), dim3(kPlanThreads), lds, s, a);
+    if (a.chunks <= kSumChunks) {
+      hipLaunchKernelGGL(k_plan_place<false>, dim3(a.chunks), dim3(kPlanThreads), lds, s, a);
+    } else {
+      hipLaunchKernelGGL(k_plan_scan, dim3(n_groups), dim3(64), 0, s, a);
+      hipLaunchKernelGGL(k_plan_place<true>, dim3(a.chunks), dim3(kPlanThreads), lds, s, a);
+    }
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EDEVICE;
 }

@@ -111,6 +111,19 @@ __device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v, int n, int 
   }
 }
 
+// Eight, added to nothing: 16 bytes of a 16-bit type at once.
+__device__ __forceinline__ void store8(void* y, int64_t at, const f32x4 (&v)[2], int n, int type) {
+  if (type != MOE_T_F32 && n >= 8) {
+    uint16_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = type == MOE_T_BF16 ? to_half<true>(v[i / 4][i % 4]) : to_half<false>(v[i / 4][i % 4]);
+    __builtin_memcpy(static_cast<uint16_t*>(y) + at, h, 16);
+  } else {
+    store4(y, at, v[0], n, type, false);
+    store4(y, at + 4, v[1], n - 4, type, false);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // work items
 // ---------------------------------------------------------------------------
@@ -318,14 +331,8 @@ struct Rows {
         const f32x4 lo = *reinterpret_cast<const MOE_LDS f32x4*>(p), hi = *reinterpret_cast<const MOE_LDS f32x4*>(p + 16);
         if (q0 + r >= q_end) continue;
         const int64_t o = (q0 + r) * ld + c0 + c;
-        if (!add && c0 + c + 8 <= cols) {
-          uint16_t h[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x = i < 4 ? lo[i] : hi[i - 4];
-            h[i] = type == MOE_T_BF16 ? to_half<true>(x) : to_half<false>(x);
-          }
-          __builtin_memcpy(static_cast<uint16_t*>(y) + o, h, 16);   // from any 2-byte boundary
+        if (!add) {
+          store8(y, o, {lo, hi}, cols - c0 - c, type);
         } else {
           store4(y, o, lo, cols - c0 - c, type, add);
           store4(y, o + 4, hi, cols - c0 - c - 4, type, add);
@@ -371,43 +378,51 @@ __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&
         rows.flush(a.pre_out + a.half, a.ld_pre, q0, q_end, c0, a.half, type, false);
       }
     } else {
-      const int l = threadIdx.x & 63, q = q0 + (l & 15), p = c0 + (l >> 4) * 4;
-      const uint16_t* gp = a.pre_in + static_cast<int64_t>(q) * a.ld_pre + p;
-      u32x2 gv[TP / 16], uv[TP / 16];
+      // dh goes through LDS; a lane then holds eight columns of a row, whose
+      // gate and up it has asked for before
+      constexpr int kPieces = (C + 31) / 32;
+      const int l = threadIdx.x & 63;
+      u32x4 gate[kPieces], up[kPieces];
 #pragma unroll
-      for (int i = 0; i < TP / 16; ++i) {
-        gv[i] = uv[i] = u32x2{0, 0};
-        if (q >= q_end) continue;
-        if (p + i * 16 + 4 <= a.np) {
-          __builtin_memcpy(&gv[i], gp + i * 16, 8);
-          __builtin_memcpy(&uv[i], gp + a.np + i * 16, 8);
+      for (int s = 0; s < kPieces; ++s) {
+        const int r = (s * 64 + l) / (C / 8), c = c0 + (s * 64 + l) % (C / 8) * 8;
+        gate[s] = up[s] = u32x4{0, 0, 0, 0};
+        if (r >= 16 || q0 + r >= q_end || c >= a.np) continue;
+        const uint16_t* at = a.pre_in + static_cast<int64_t>(q0 + r) * a.ld_pre + c;
+        if (c + 8 <= a.np) {
+          __builtin_memcpy(&gate[s], at, 16);
+          __builtin_memcpy(&up[s], at + a.np, 16);
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (p + i * 16 + e < a.np) {
-              gv[i][e / 2] |= static_cast<uint32_t>(gp[i * 16 + e]) << 16 * (e & 1);
-              uv[i][e / 2] |= static_cast<uint32_t>(gp[a.np + i * 16 + e]) << 16 * (e & 1);
+          for (int e = 0; e < 8; ++e)
+            if (c + e < a.np) {
+              gate[s][e / 2] |= static_cast<uint32_t>(at[e]) << 16 * (e & 1);
+              up[s][e / 2] |= static_cast<uint32_t>(at[a.np + e]) << 16 * (e & 1);
             }
         }
       }
 #pragma unroll
-      for (int i = 0; i < TP / 16; ++i) {
-        f32x4 dg;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float g = from_half<BF>(static_cast<uint16_t>(gv[i][e / 2] >> 16 * (e & 1)));
-          const float u = from_half<BF>(static_cast<uint16_t>(uv[i][e / 2] >> 16 * (e & 1)));
-          const float s = 1.0f / (1.0f + __expf(-g)), dh = acc[i][j][e];
-          dg[e] = dh * u * s * (1.0f + g * (1.0f - s));
-          acc[i][j][e] = dh * g * s;
-        }
-        rows.put(i, dg);
-      }
-      rows.flush(y, a.ldy, q0, q_end, c0, a.np, a.out_type, false);
-#pragma unroll
       for (int i = 0; i < TP / 16; ++i) rows.put(i, acc[i][j]);
-      rows.flush(static_cast<uint8_t*>(y) + static_cast<int64_t>(a.np) * (a.out_type == MOE_T_F32 ? 4 : 2), a.ldy, q0, q_end,
-                c0, a.np, a.out_type, false);
+      uint8_t* y2 = static_cast<uint8_t*>(y) + static_cast<int64_t>(a.np) * (a.out_type == MOE_T_F32 ? 4 : 2);
+#pragma unroll
+      for (int s = 0; s < kPieces; ++s) {
+        const int r = (s * 64 + l) / (C / 8), cl = (s * 64 + l) % (C / 8) * 8, c = c0 + cl;
+        if (r >= 16 || q0 + r >= q_end || c >= a.np) continue;
+        const MOE_LDS uint8_t* at = rows.at + r * rows.kPitch + cl * 4;
+        f32x4 dh[2], dg[2], du[2];
+        dh[0] = *reinterpret_cast<const MOE_LDS f32x4*>(at);
+        dh[1] = *reinterpret_cast<const MOE_LDS f32x4*>(at + 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float g = from_half<BF>(static_cast<uint16_t>(gate[s][e / 2] >> 16 * (e & 1)));
+          const float u = from_half<BF>(static_cast<uint16_t>(up[s][e / 2] >> 16 * (e & 1)));
+          const float sg = 1.0f / (1.0f + __expf(-g)), d = dh[e / 4][e % 4];
+          dg[e / 4][e % 4] = d * u * sg * (1.0f + g * (1.0f - sg));
+          du[e / 4][e % 4] = d * g * sg;
+        }
+        const int64_t o = (q0 + r) * a.ldy + c;
+        store8(y, o, dg, a.np - c, a.out_type);
+        store8(y2, o, du, a.np - c, a.out_type);
+      }
     }
   }
 }
@@ -471,18 +486,40 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
   }
 
   u32x4 vp[NP], vq[NQ];
+  [[maybe_unused]] int from[NP];   // gathered: the chunks' rows of the next step to fetch, -1 for none
+  const auto look_up = [&](int r0) {
+    if constexpr (kWeight) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int r = r0 + (tid + i * NT) / (BP / 8);
+        from[i] = r < red ? source_row(a, it.begin + r) : -1;
+      }
+    }
+  };
   const auto fetch = [&](int r0) {
     // A step whose chunks all lie inside their operands needs no care.  An
     // across chunk may run past its row there: the columns past the last
     // belong to no output.
-    const bool inner = r0 + kRed <= red && (!PA || (!gather && pbase + (r0 + kRed - 1) * a.ldp + it.p0 + BP <= pend)) &&
+    const bool inner = r0 + kRed <= red &&
+                       (!PA || (gather ? it.p0 + BP <= a.np : pbase + (r0 + kRed - 1) * a.ldp + it.p0 + BP <= pend)) &&
                        (!QA || qbase + (r0 + kRed - 1) * a.ldq + it.q0 + BQ <= qend);
     const int64_t po = PA ? r0 * a.ldp : r0, qo = QA ? r0 * a.ldq : r0;
     if (inner) {
+      if (gather) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) __builtin_memcpy(&vp[i], ps[i] + po, 16);
+        for (int i = 0; i < NP; ++i)
+          __builtin_memcpy(&vp[i], pbase + (from[i] < 0 ? 0 : from[i]) * a.ldp + it.p0 + (tid + i * NT) % (BP / 8) * 8, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) __builtin_memcpy(&vp[i], ps[i] + po, 16);
+      }
 #pragma unroll
       for (int i = 0; i < NQ; ++i) __builtin_memcpy(&vq[i], qs[i] + qo, 16);
+      if (gather) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          if (from[i] < 0) vp[i] = u32x4{0, 0, 0, 0};
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -494,9 +531,8 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
           const uint16_t* s = ps[i] + po;
           bool in = r < red;
           if (gather) {
-            const int row = in ? source_row(a, it.begin + r) : -1;
-            in = row >= 0;
-            s = pbase + row * a.ldp + a.np - cols;
+            in = from[i] >= 0;
+            s = pbase + from[i] * a.ldp + a.np - cols;
           }
           vp[i] = load8(s, pend, !in ? 0 : s + 8 <= pend ? 8 : cols);
         }
@@ -519,8 +555,10 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_any(Gemm a) {
           if (none >> i & 1) vq[i] = u32x4{0, 0, 0, 0};
       }
     }
+    if (gather) look_up(r0 + kRed);
   };
 
+  if (gather) look_up(0);
   fetch(0);
   for (int r0 = 0; r0 < red; r0 += kRed) {
     __syncthreads();
@@ -589,7 +627,7 @@ struct Feed {
 
   // Tile row (straight: of the tile, across: of the step) that load i of this lane fetches.
   static __device__ __forceinline__ int row(int i) {
-    const int l = threadIdx.x & 63, w = wave_id();
+    const int l = threadIdx.x & 63, w = wave_id() % WAVES;
     return (w * N + i) * kRowsPerLoad + (ACROSS ? l / (B / 8) : l >> 3);
   }
   // Across: the column of the chunk that load i of this lane fetches.
@@ -601,7 +639,7 @@ struct Feed {
 
   // Straight operands and across operands without a gather.
   __device__ __forceinline__ void load(MOE_LDS uint8_t* tile, int t) const {
-    const int w = wave_id(), left = red - t * kRed;
+    const int w = wave_id() % WAVES, left = red - t * kRed;
     MOE_LDS uint8_t* at = tile + w * N * 1024;
     if (ACROSS || left >= kRed) {
 #pragma unroll
@@ -622,19 +660,23 @@ __device__ __forceinline__ void step_barrier() {
   else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
 }
 
-template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ, int STAGES>
-__global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
+// SPLIT > 1: few tiles with a long contraction.  SPLIT groups of WP x WQ waves
+// take the steps in turn, each with its own part of a stage, and the groups'
+// sums are added in order at the end.
+template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ, int STAGES, int SPLIT>
+__global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
   constexpr int TP = BP / WP, TQ = BQ / WQ, NW = WP * WQ;
   constexpr bool kWeight = PA && QA;   // wgrad
-  constexpr int kStage = (BP + BQ) * 128;
-  static_assert(NW * Rows<TP>::kBytes <= STAGES * kStage, "the epilogue's rows use the tiles' memory");
+  constexpr int kStep = (BP + BQ) * 128, kStage = SPLIT * kStep;
+  static_assert(SPLIT == 1 || (SPLIT - 1) * BP * BQ * 4 <= STAGES * kStage, "the groups' sums use the tiles' memory");
+  static_assert(NW * Rows<TP>::kBytes + (SPLIT - 1) * BP * BQ * 4 <= STAGES * kStage, "the epilogue's rows use the tiles' memory");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * kStage];
   const Item it = kWeight ? find_matrix<BP, BQ>(a) : find_rows<BP, BQ>(a);
   if (!it.any) return;
-  const int wave = wave_id(), wp = wave % WP, wq = wave / WP;
+  const int wave = wave_id() % NW, turn = wave_id() / NW, wp = wave % WP, wq = wave / WP;
   const int red = kWeight ? it.end - it.begin : a.nr;
   const int q_end = kWeight ? a.nq : it.end;
-  MOE_LDS uint8_t* base = (MOE_LDS uint8_t*)lds;
+  MOE_LDS uint8_t* base = (MOE_LDS uint8_t*)lds + turn * kStep;   // stages are kStage apart
 
   Feed<PA, BP, NW> fp;
   Feed<QA, BQ, NW> fq;
@@ -694,10 +736,12 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
       }
     }
   };
-  if (kWeight && a.src) fetch(0);
+  if (kWeight && a.src) fetch(turn);
 
-  const auto issue = [&](int t) {
-    MOE_LDS uint8_t* tp = base + t % STAGES * kStage;
+  // stage m holds steps m * SPLIT .. ; this group's is `turn` of them
+  const auto issue = [&](int m) {
+    const int t = m * SPLIT + turn;
+    MOE_LDS uint8_t* tp = base + m % STAGES * kStage;
     if (kWeight && a.src) {
       const int sub = (threadIdx.x & 63) / (BP / 8);   // which of a load's rows
 #pragma unroll
@@ -711,7 +755,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
         }
         to_lds(fp.buf, tp + (wave * fp.N + i) * 1024, off + fp.lane[i], 0);
       }
-      fetch(t + 1);
+      fetch(t + SPLIT);
     } else {
       fp.load(tp, t);
     }
@@ -734,8 +778,8 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
 #pragma unroll
       for (int j = 0; j < TQ / 16; ++j) acc[i][j] = mma<BF>(vp[i], vq[j], acc[i][j]);
   };
-  const int steps = (red + kRed - 1) / kRed;
-  if constexpr (STAGES == 2 && NW == 8) {
+  const int steps = (red + kRed * SPLIT - 1) / (kRed * SPLIT);
+  if constexpr (STAGES == 2 && NW == 8 && SPLIT == 1) {
     // Two waves share a SIMD, and four of the eight run one phase behind the
     // other four: while one wave of a SIMD multiplies, the other one reads its
     // next fragments and issues loads, so the matrix cores see no gap.  A step
@@ -781,6 +825,28 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_group_tiles(Gemm a) {
     }
   }
   step_barrier<0>();
+  base = (MOE_LDS uint8_t*)lds;
+  if constexpr (SPLIT > 1) {
+    // [group - 1][wave][fragment][lane]
+    constexpr int kFragments = TP / 16 * (TQ / 16);
+    MOE_LDS f32x4* sums = reinterpret_cast<MOE_LDS f32x4*>(base) + wave * kFragments * 64 + (threadIdx.x & 63);
+    if (turn) {
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ / 16; ++j) sums[((turn - 1) * NW * kFragments + i * (TQ / 16) + j) * 64] = acc[i][j];
+    }
+    __syncthreads();
+    if (turn) return;
+#pragma unroll
+    for (int s = 1; s < SPLIT; ++s)
+#pragma unroll
+      for (int i = 0; i < TP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ / 16; ++j) acc[i][j] += sums[((s - 1) * NW * kFragments + i * (TQ / 16) + j) * 64];
+    // the epilogue's rows may lie over another wave's sums
+    base += (SPLIT - 1) * BP * BQ * 4;
+  }
   void* y = a.y;
   if constexpr (kWeight) y = static_cast<uint8_t*>(y) + it.group * a.y_stride * (a.out_type == MOE_T_F32 ? 4 : 2);
   epilogue<BF, EPI, TP, TQ>(a, it, acc, wp, wq, q_end, y, base);
@@ -824,13 +890,13 @@ int64_t grid_of(Gemm& a, int BP, int BQ) {
   return grid > kMaxGrid ? 0 : grid;
 }
 
-template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ, int STAGES>
+template <bool BF, bool PA, bool QA, int EPI, int BP, int BQ, int WP, int WQ, int STAGES, int SPLIT = 1>
 int go(Gemm a, hipStream_t s) {
   const int64_t grid = grid_of<PA && QA, EPI>(a, BP, BQ);
   if (!grid) return MOE_ESHAPE;
-  const dim3 g(static_cast<uint32_t>(grid)), b(64 * WP * WQ);
+  const dim3 g(static_cast<uint32_t>(grid)), b(64 * WP * WQ * SPLIT);
   if constexpr (STAGES == 0) hipLaunchKernelGGL((k_group_any<BF, PA, QA, EPI, BP, BQ, WP, WQ>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((k_group_tiles<BF, PA, QA, EPI, BP, BQ, WP, WQ, STAGES>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((k_group_tiles<BF, PA, QA, EPI, BP, BQ, WP, WQ, STAGES, SPLIT>), g, b, 0, s, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EDEVICE;
 }
 
@@ -854,19 +920,26 @@ int go(Gemm a, hipStream_t s) {
 // and for weight gradients (64x64 in the last column)
 //     8192 x 1024 x 1024 (1)         178      122     100      85
 //     16384 x 5120 x 2304 (16)       441      525     587     728
+// The last entry of each table is the small tile with its steps dealt to four
+// groups of waves: 16 x 512 x 8192 34 -> 20 us, 64 x 4096 x 4096 19 -> 13, the
+// weight gradient of 8192 x 1024 x 1024 85 -> 42; with many tiles it loses (512 x
+// 4096 x 4096 39 -> 51), one workgroup filling a compute unit.
 struct TileCost {
   int bp, bq;
   double fixed, latency, step;
   int fit;
   double bandwidth;
 };
-enum { kLarge, kMedium, kFlat, kSmall };
+enum { kLarge, kMedium, kFlat, kSmall, kDeep };
 constexpr TileCost kStraightCost[] = {{256, 256, 10, 1.15, 1.5, 1, 4.4}, {128, 128, 8, 0.58, 0.537, 2, 5.3},
-                                      {128, 64, 4, 0.5, 0.33, 3, 5.0}, {64, 32, 3, 0.25, 0.144, 3, 5.3}};
+                                      {128, 64, 4, 0.5, 0.33, 3, 5.0}, {64, 32, 3, 0.25, 0.144, 3, 5.3},
+                                      {64, 32, 5, 0.12, 0.12, 1, 5.0}};
 constexpr TileCost kAcrossCost[] = {{256, 256, 10, 1.25, 1.4, 1, 4.2}, {128, 128, 8, 0.82, 0.62, 2, 5.0},
-                                    {128, 64, 4, 0.67, 0.36, 3, 4.8}, {64, 32, 3, 0.5, 0.21, 3, 4.5}};
-constexpr TileCost kWeightCost[] = {{256, 256, 10, 1.25, 1.6, 1, 5.0}, {128, 128, 8, 0.85, 0.75, 2, 5.0},
-                                    {128, 64, 4, 0.75, 0.42, 3, 5.0}, {64, 64, 3, 0.63, 0.25, 5, 5.0}};
+                                    {128, 64, 4, 0.67, 0.36, 3, 4.8}, {64, 32, 3, 0.5, 0.21, 3, 4.5},
+                                    {64, 32, 5, 0.2, 0.2, 1, 4.5}};
+constexpr TileCost kWeightCost[] = {{256, 256, 9.2, 1.25, 1.6, 1, 5.0}, {128, 128, 5.2, 0.85, 0.75, 2, 5.0},
+                                    {128, 64, 4, 0.75, 0.42, 3, 5.0}, {64, 64, 3.7, 0.63, 0.25, 5, 5.0},
+                                    {64, 64, 4, 0.28, 0.28, 1, 5.0}};
 
 // The register path, any operands:
 //     8192 x 2303 x 5121 (8)         128x128 353, 64x64 599; gradients 343 / 560 and 317 / 511
@@ -901,7 +974,7 @@ int tile_shape(const Gemm& a, const TileCost (&costs)[N]) {
     const double chain = rounds * c.latency, work = per_cu * c.step;
     double t = rounds * c.fixed + steps * (chain > work ? chain : work);
     // weight gradients: the tiles of a group with four times the mean rows end last
-    if (kWeight && a.groups > 1) t += 3 * steps * c.latency;
+    if (kWeight) t += (a.groups < 4 ? a.groups - 1 : 3) * steps * c.latency;
     t = t > bytes ? t + bytes / 4 : bytes + t / 4;
     if (i == 0 || t < least) {
       best = i;
@@ -921,9 +994,12 @@ int launch(const Gemm& a, hipStream_t s) {
     case kLarge: return go<BF, PA, QA, EPI, 256, 256, 2, 4, 2>(a, s);
     case kMedium: return go<BF, PA, QA, EPI, 128, 128, 2, 2, 2>(a, s);
     case kFlat: return go<BF, PA, QA, EPI, 128, 64, 2, 2, 2>(a, s);
-    default:
+    case kSmall:
       if constexpr (PA && QA) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 2>(a, s);
       else return go<BF, PA, QA, EPI, 64, 32, 2, 2, 4>(a, s);
+    default:
+      if constexpr (PA && QA) return go<BF, PA, QA, EPI, 64, 64, 2, 2, 2, 4>(a, s);
+      else return go<BF, PA, QA, EPI, 64, 32, 2, 2, 3, 4>(a, s);
   }
 }
 
