@@ -415,15 +415,17 @@ _types = {}
 
 
 def _type_of(t):
-    if not _types:
+    code = _types.get(t.dtype)
+    if code is None and not _types:
         import torch
         _types.update({torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16, torch.int32: -1})
-    return _types.get(t.dtype)
+        code = _types.get(t.dtype)
+    return -2 if code is None else code
 
 
 def _type(fn, t):
     code = _type_of(t)
-    if code is None or code < 0:
+    if code < 0:
         raise MoeError(fn, MOE_EFORMAT)
     return code
 
@@ -433,21 +435,35 @@ def _need(fn, ok, status=MOE_ESHAPE):
         raise MoeError(fn, status)
 
 
-def _addresses(fn, *tensors):
-    """Addresses of tensors (None: None) that have to lie on the current device."""
+_hooks = None
+
+
+def _device_hooks():
+    """(current device, current raw stream of a device): torch's own cheap forms of both where it has them."""
+    global _hooks
+    import torch
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _hooks = (device, stream)
+    return _hooks
+
+
+def _addresses(fn, stream, *tensors):
+    """The stream's handle, then the addresses of tensors (None: None) that have to lie on the current device."""
     dev = tensors[0].get_device()
-    if dev >= 0:
-        import torch
-        if dev != torch.cuda.current_device():
-            dev = -1
-    out = []
+    if dev < 0:
+        raise MoeError(fn, MOE_EINVAL)
+    device, current = _hooks or _device_hooks()
+    if dev != device():
+        raise MoeError(fn, MOE_EINVAL)
+    out = [current(dev) if stream is None else stream.cuda_stream]
     for t in tensors:
         if t is None:
             out.append(None)
-            continue
-        if dev < 0 or t.get_device() != dev:
+        elif t.get_device() != dev:
             raise MoeError(fn, MOE_EINVAL)
-        out.append(t.data_ptr())
+        else:
+            out.append(t.data_ptr())
     return out
 
 
@@ -476,7 +492,7 @@ def moe_group_plan(idx, n_groups, offsets, pairs, pos, ws=None, stream=None):
     """idx [rows, top_k] int32 -> offsets [n_groups + 1], pairs and pos [rows * top_k] (all int32);
     ws: group_plan_bytes(rows, top_k, n_groups) bytes, or None when that is 0."""
     fn = "moe_group_plan"
-    at = _addresses(fn, idx, offsets, pairs, pos, ws)
+    st, *at = _addresses(fn, stream, idx, offsets, pairs, pos, ws)
     _need(fn, idx.dim() == 2)
     rows, top_k = idx.shape
     n = rows * top_k
@@ -484,7 +500,7 @@ def moe_group_plan(idx, n_groups, offsets, pairs, pos, ws=None, stream=None):
         _ints(fn, t, count)
     _need(fn, ws is None or ws.is_contiguous())
     _check(fn, lib().moe_group_plan(at[0], rows, top_k, int(n_groups), at[1], at[2], at[3], at[4],
-                                    0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+                                    0 if ws is None else ws.numel() * ws.element_size(), st))
 
 
 def _group_dims(fn, x, src, src_div, offsets, rows, w, out_type):
@@ -505,7 +521,7 @@ def _group_dims(fn, x, src, src_div, offsets, rows, w, out_type):
 
 def _product(fn, call, x, offsets, w, y, src, src_div, back, stream, pre=None, factor=None):
     """factor: None without pre, else the columns of (y, pre) per column of the product, times two."""
-    xa, oa, wa, ya, sa, pa = _addresses(fn, x, offsets, w, y, src, pre)
+    s, xa, oa, wa, ya, sa, pa = _addresses(fn, stream, x, offsets, w, y, src, pre)
     rows, y_cols, ldy = _rows(fn, y)
     d, x_cols = _group_dims(fn, x, src, src_div, offsets, rows, w, _type(fn, y))
     d.ldy = ldy
@@ -514,14 +530,13 @@ def _product(fn, call, x, offsets, w, y, src, src_div, back, stream, pre=None, f
         raise MoeError(fn, MOE_ESHAPE)
     d_ref = ctypes.byref(d)
     if factor is None:
-        st = call(d_ref, xa, sa, oa, wa, ya, _stream(stream))
+        st = call(d_ref, xa, sa, oa, wa, ya, s)
     else:
         if pre is not None:
             p_rows, p_cols, d.ld_pre = _rows(fn, pre)
             if pre.dtype != x.dtype or p_rows != rows or 2 * p_cols != cols * factor[1]:
                 raise MoeError(fn, MOE_ESHAPE)
-        st = call(d_ref, xa, sa, oa, wa, pa, ya, _stream(stream)) if back else \
-            call(d_ref, xa, sa, oa, wa, ya, pa, _stream(stream))
+        st = call(d_ref, xa, sa, oa, wa, pa, ya, s) if back else call(d_ref, xa, sa, oa, wa, ya, pa, s)
     _check(fn, st)
 
 
@@ -552,13 +567,13 @@ def moe_group_swiglu_grad(dy, offsets, w, pre, dpre, src=None, src_div=1, stream
 def moe_group_wgrad(dy, x, offsets, dw, src=None, src_div=1, accumulate=False, stream=None):
     """dw [groups, n, k] = (or +=) dy[rows of the group]^T x[src // src_div of those rows]."""
     fn = "moe_group_wgrad"
-    dya, xa, oa, dwa, sa = _addresses(fn, dy, x, offsets, dw, src)
+    s, dya, xa, oa, dwa, sa = _addresses(fn, stream, dy, x, offsets, dw, src)
     rows, n, ldy = _rows(fn, dy)
     d, x_cols = _group_dims(fn, x, src, src_div, offsets, rows, dw, _type(fn, dw))
     d.ldy = ldy
     if dy.dtype != x.dtype or x_cols != d.k or n != d.n:
         raise MoeError(fn, MOE_ESHAPE)
-    _check(fn, lib().moe_group_wgrad(ctypes.byref(d), dya, xa, sa, oa, dwa, 1 if accumulate else 0, _stream(stream)))
+    _check(fn, lib().moe_group_wgrad(ctypes.byref(d), dya, xa, sa, oa, dwa, 1 if accumulate else 0, s))
 
 
 def _combine_dims(fn, o_rows, ldo, y, pos, wts, top_k, in_type, out_type):
@@ -579,19 +594,19 @@ def _top_k(fn, rows, pos, wts, o_rows, top_k):
 def moe_group_combine(o, pos, wts, y, top_k=None, stream=None):
     """y [rows, n] = sum over a row's top_k pairs of wts * o[pos]; pos None: pair p is row p; wts None: 1."""
     fn = "moe_group_combine"
-    oa, pa, wa, ya = _addresses(fn, o, pos, wts, y)
+    s, oa, pa, wa, ya = _addresses(fn, stream, o, pos, wts, y)
     kind, out = _type(fn, o), _type(fn, y)
     o_rows, n, ldo = _rows(fn, o)
     d = _combine_dims(fn, o_rows, ldo, y, pos, wts, _top_k(fn, y.shape[0], pos, wts, o_rows, top_k), kind, out)
     _need(fn, d.n == n)
-    _check(fn, lib().moe_group_combine(ctypes.byref(d), oa, pa, wa, ya, _stream(stream)))
+    _check(fn, lib().moe_group_combine(ctypes.byref(d), oa, pa, wa, ya, s))
 
 
 def moe_group_combine_grad(dy, o, pos, wts, d_o, d_wts, top_k=None, stream=None):
     """d_o[pos] = wts * dy (rows of d_o that no pair names stay as they were) and d_wts = <dy, o[pos]>; either
     output may be None.  o (None without d_wts) and d_o have the same row stride."""
     fn = "moe_group_combine_grad"
-    dya, oa, pa, wa, doa, dwa = _addresses(fn, dy, o, pos, wts, d_o, d_wts)
+    s, dya, oa, pa, wa, doa, dwa = _addresses(fn, stream, dy, o, pos, wts, d_o, d_wts)
     like = d_o if d_o is not None else o
     _need(fn, like is not None and (d_wts is None or o is not None), MOE_EINVAL)
     kind, out = _type(fn, dy), _type(fn, like)
@@ -603,7 +618,7 @@ def moe_group_combine_grad(dy, o, pos, wts, d_o, d_wts, top_k=None, stream=None)
     _need(fn, d.n == n)
     if d_wts is not None:
         _need(fn, _type(fn, d_wts) == T_F32 and d_wts.is_contiguous() and d_wts.shape == (d.rows, top_k))
-    _check(fn, lib().moe_group_combine_grad(ctypes.byref(d), dya, oa, pa, wa, doa, dwa, _stream(stream)))
+    _check(fn, lib().moe_group_combine_grad(ctypes.byref(d), dya, oa, pa, wa, doa, dwa, s))
 
 
 # ----------------------------------------------------------------------------- 4-bit matrix-vector products
@@ -640,7 +655,7 @@ def moe_q4_matvec(x, codes, scales, zeros, group, y, idx=None, x_div=1, swiglu=F
     W = (gate | up), y = silu(gate) * up.  codes / scales / zeros (or None): the packed matrices back to back;
     n_mats defaults to the first dimension of codes when it has more than one, else 1."""
     fn = "moe_q4_matvec"
-    xa, ca, sa, za, ya, ia = _addresses(fn, x, codes, scales, zeros, y, idx)
+    s, xa, ca, sa, za, ya, ia = _addresses(fn, stream, x, codes, scales, zeros, y, idx)
     kind, out = _type(fn, x), _type(fn, y)
     x_rows, k, ldx = _rows(fn, x)
     rows, n, ldy = _rows(fn, y)
@@ -655,7 +670,7 @@ def moe_q4_matvec(x, codes, scales, zeros, group, y, idx=None, x_div=1, swiglu=F
         if t is not None and (t.numel() * t.element_size() < need * n_mats or not t.is_contiguous()):
             raise MoeError(fn, MOE_ESHAPE)
     d = Q4Dims(n, k, group, n_mats, rows, x_div, kind, out, 1 if swiglu else 0, ldx, ldy)
-    _check(fn, lib().moe_q4_matvec(ctypes.byref(d), xa, ia, ca, sa, za, ya, _stream(stream)))
+    _check(fn, lib().moe_q4_matvec(ctypes.byref(d), xa, ia, ca, sa, za, ya, s))
 
 
 @functools.lru_cache(maxsize=256)
