@@ -13,6 +13,7 @@ namespace grp {
 
 using dev::u32x2;
 using dev::u32x4;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
 // Dispatch: a stable counting sort of the pairs by expert id.
@@ -262,7 +263,8 @@ __device__ __forceinline__ void store_v(void* base, int64_t at, const float (&v)
     float* p = static_cast<float*>(base) + at;
     if constexpr (V >= 4) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = float4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      for (int i = 0; i < V; i += 4)
+        __builtin_nontemporal_store(f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]}, reinterpret_cast<f32x4*>(p + i));
     } else {
       p[0] = v[0];
     }
@@ -277,11 +279,11 @@ __device__ __forceinline__ void store_v(void* base, int64_t at, const float (&v)
   if constexpr (V == 8) {
     u32x4 q;
     __builtin_memcpy(&q, h, 16);
-    *reinterpret_cast<u32x4*>(p) = q;
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(p));
   } else if constexpr (V == 4) {
     u32x2 q;
     __builtin_memcpy(&q, h, 8);
-    *reinterpret_cast<u32x2*>(p) = q;
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(p));
   } else {
     p[0] = h[0];
   }

@@ -78,8 +78,15 @@ __device__ __forceinline__ float from_half(uint16_t v) {
   else return static_cast<float>(__builtin_bit_cast(_Float16, v));
 }
 
-// Four consecutive outputs, of which `n` exist.  Whole pieces go out as one
-// vector, from any element boundary.
+// Vectors at any element boundary.  Outputs are stored past the caches' usual
+// order: kept in it, a large output pushes out the operands that other tiles
+// will read again (the fp32 weight gradients of 16 experts of 4608 x 5120: 1024
+// us, 930 so).
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+
+// Four consecutive outputs, of which `n` exist.
 __device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v, int n, int type, bool add) {
   if (type == MOE_T_F32) {
     float* o = static_cast<float*>(y) + at;
@@ -89,7 +96,7 @@ __device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v, int n, int 
         __builtin_memcpy(&held, o, 16);
         v += held;
       }
-      __builtin_memcpy(o, &v, 16);
+      __builtin_nontemporal_store(v, reinterpret_cast<f32x4_any*>(o));
     } else {
       for (int i = 0; i < 4; ++i)
         if (i < n) o[i] = add ? o[i] + v[i] : v[i];
@@ -104,7 +111,9 @@ __device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v, int n, int 
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = type == MOE_T_BF16 ? to_half<true>(v[i]) : to_half<false>(v[i]);
   if (n >= 4) {
-    __builtin_memcpy(o, h, 8);
+    u32x2 w;
+    __builtin_memcpy(&w, h, 8);
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x2_any*>(o));
   } else {
     for (int i = 0; i < 4; ++i)
       if (i < n) o[i] = h[i];
@@ -117,7 +126,9 @@ __device__ __forceinline__ void store8(void* y, int64_t at, const f32x4 (&v)[2],
     uint16_t h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = type == MOE_T_BF16 ? to_half<true>(v[i / 4][i % 4]) : to_half<false>(v[i / 4][i % 4]);
-    __builtin_memcpy(static_cast<uint16_t*>(y) + at, h, 16);
+    u32x4 w;
+    __builtin_memcpy(&w, h, 16);
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any*>(static_cast<uint16_t*>(y) + at));
   } else {
     store4(y, at, v[0], n, type, false);
     store4(y, at + 4, v[1], n - 4, type, false);
