@@ -734,8 +734,10 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
   // vector-memory count waits for), a step before they are used.
   constexpr int kR = PA ? Feed<PA, BP, NW>::kRowsPerLoad : 1, kNext = decltype(fp)::N * kR;
   [[maybe_unused]] int32_t next[kNext];
-  const auto fetch = [&](int t) {
+  const auto fetch = [&](int m) {
     if constexpr (kWeight) {
+      if (!a.src) return;
+      const int t = m * SPLIT + turn;
       const int first = it.begin + t * kRed + wave * kNext;
       const ConstInts src = reinterpret_cast<ConstInts>(reinterpret_cast<uintptr_t>(a.src));
       if (first + kNext <= it.end) {
@@ -747,7 +749,7 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
       }
     }
   };
-  if (kWeight && a.src) fetch(turn);
+  fetch(0);
 
   // stage m holds steps m * SPLIT .. ; this group's is `turn` of them
   const auto issue = [&](int m) {
@@ -766,7 +768,6 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
         }
         to_lds(fp.buf, tp + (wave * fp.N + i) * 1024, off + fp.lane[i], 0);
       }
-      fetch(t + SPLIT);
     } else {
       fp.load(tp, t);
     }
@@ -801,6 +802,7 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
     // the others in their third phase, which ends at the same barrier.
     const bool behind = wave >= 4;
     issue(0);
+    fetch(1);
     step_barrier<0>();
     if (behind) asm volatile("s_barrier" ::: "memory");
     for (int t = 0; t < steps; ++t) {
@@ -810,6 +812,7 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
         if (kk == 0) issue(t + 1);
         if (kk == 1 && behind) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (kk == 0) fetch(t + 2);   // waited for with the next fragments, a phase from here
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
         multiply();
@@ -824,10 +827,14 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
     // steps past the last read nothing (every lane is outside), so the number
     // of loads in flight is the same at every barrier
 #pragma unroll
-    for (int t = 0; t < STAGES - 1; ++t) issue(t);
+    for (int t = 0; t < STAGES - 1; ++t) {
+      issue(t);
+      fetch(t + 1);
+    }
     for (int t = 0; t < steps; ++t) {
       step_barrier<(STAGES - 2) * (decltype(fp)::N + decltype(fq)::N)>();
       issue(t + STAGES - 1);
+      fetch(t + STAGES);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         read(t, kk);
