@@ -241,6 +241,114 @@ def test_offsets_out_of_range_are_clamped():
         assert bool((y[torch.from_numpy(~m).cuda()] == SENTINEL).all())
 
 
+# ----------------------------------------------------------------------------- large
+def _device_reference(way, x, w, bounds, src=None, div=1):
+    """fp64 on the GPU: the same definitions for sizes that take the large tiles."""
+    xs = x if src is None else x[(src.long() // div)]
+    parts = []
+    for g in range(len(bounds) - 1):
+        a = xs[bounds[g]:bounds[g + 1]].double()
+        parts.append(a @ (w[g].double() if way == "t" else w[g].double().t().contiguous()))
+    return torch.cat(parts)
+
+
+LARGE = [([2048, 0, 1700, 333], 4608, 520), ([600] * 8, 2304, 264), ([5000], 1536, 1032), ([40] * 96, 1280, 512)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("shape", range(len(LARGE)))
+def test_large_products_and_gradients(shape, gather):
+    """Every call at sizes of many tiles, bf16, against fp64 products on the GPU: relative error of the whole
+    within half a bf16 step (2^-8) and of fp32 outputs within T * 2^-24 for T terms of like size."""
+    counts, n, k = LARGE[shape]
+    gen = torch.Generator(device="cuda").manual_seed(shape)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(BF16)  # noqa: E731
+    groups, rows = len(counts), sum(counts)
+    bounds = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    off = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    x, w, dy = r(rows // 2 if gather else rows, k), r(groups, n, k) * 0.05, r(rows, n)
+    src = torch.randint(0, 2 * x.shape[0], (rows,), generator=gen, device="cuda").int() if gather else None
+    kw = dict(src=src, src_div=2) if gather else {}
+
+    def near(got, ref, tol):
+        err = float((got.double() - ref).norm() / ref.norm())
+        assert err <= tol, err
+        worst = float(((got.double() - ref).abs() / (ref.abs() + ref.abs().mean())).max())
+        assert worst <= 4 * tol + 1e-5, worst
+
+    y = torch.empty(rows, n, dtype=BF16, device="cuda")
+    L.moe_group_matmul(x, off, w, y, **kw)
+    ref = _device_reference("n", x, w, bounds, src, 2)
+    near(y, ref, 2.0**-8)
+    h, pre = torch.empty(rows, n // 2, dtype=BF16, device="cuda"), torch.empty_like(y)
+    L.moe_group_swiglu(x, off, w, h, pre=pre, **kw)
+    g, u = ref.chunk(2, 1)
+    near(pre, ref, 2.0**-8)
+    near(h, torch.nn.functional.silu(g) * u, 2.0**-8)
+    dx = torch.empty(rows, k, device="cuda")
+    L.moe_group_matmul_t(dy, off, w, dx)
+    ref = _device_reference("t", dy, w, bounds)
+    near(dx, ref, n * 2.0**-24)
+    pre2, dpre = r(rows, 2 * k), torch.empty(rows, 2 * k, dtype=BF16, device="cuda")
+    L.moe_group_swiglu_grad(dy, off, w, pre2, dpre)
+    g, u = pre2.double().chunk(2, 1)
+    s = torch.sigmoid(g)
+    near(dpre, torch.cat([ref * u * (s + g * s * (1 - s)), ref * g * s], 1), 2.0**-8)
+    dw = torch.empty(groups, n, k, device="cuda")
+    L.moe_group_wgrad(dy, x, off, dw, **kw)
+    xs = x if src is None else x[src.long() // 2]
+    ref = torch.stack([dy[a:b].double().t().contiguous() @ xs[a:b].double() for a, b in zip(bounds, bounds[1:])])
+    near(dw, ref, max(counts) * 2.0**-24)
+    again = torch.empty_like(dw)
+    L.moe_group_wgrad(dy, x, off, again, **kw)
+    assert torch.equal(dw, again)
+
+
+def test_operands_past_32_bit_offsets():
+    """x and y of 4.9 GB, rows picked from both ends."""
+    rows, wide, narrow = 600_000, 4096, 64
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.zeros(rows, wide, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 7, 262_143, 262_144, 524_287, 524_288, rows - 1], device="cuda")
+    x[at] = torch.randn(len(at), wide, generator=gen, device="cuda").to(BF16)
+    w = (torch.randn(2, narrow, wide, generator=gen, device="cuda") * 0.05).to(BF16)
+    src, off = at.int(), torch.tensor([0, 3, len(at)], dtype=torch.int32, device="cuda")
+    y = torch.empty(len(at), narrow, device="cuda")
+    L.moe_group_matmul(x, off, w, y, src=src)
+    ref = torch.cat([x[at[:3]].double() @ w[0].double().t().contiguous(), x[at[3:]].double() @ w[1].double().t().contiguous()])
+    _close(y, _f64(ref), np.abs(_f64(ref)) * 1e-5 + wide * 2.0**-24 * 4, "gathered from far rows")
+    # all rows: the whole x, then its gradients
+    off = torch.tensor([0, 524_280, rows], dtype=torch.int32, device="cuda")
+    y = torch.empty(rows, narrow, device="cuda")
+    L.moe_group_matmul(x, off, w, y)
+    group = (at >= 524_280).long()
+    ref = torch.stack([w[g].double() @ x[i].double() for g, i in zip(group.tolist(), at.tolist())])
+    _close(y[at], _f64(ref), np.abs(_f64(ref)) * 1e-5 + wide * 2.0**-24 * 4, "rows past 4 GB")
+    assert int((y != 0).any(1).sum()) == len(at)
+    dy = torch.zeros(rows, narrow, dtype=BF16, device="cuda")
+    dy[at] = torch.randn(len(at), narrow, generator=gen, device="cuda").to(BF16)
+    dw = torch.empty(2, narrow, wide, device="cuda")
+    L.moe_group_wgrad(dy, x, off, dw)
+    ref = torch.stack([dy[at][group == g].double().t().contiguous() @ x[at][group == g].double() for g in (0, 1)])
+    _close(dw, _f64(ref), np.abs(_f64(ref)) * 1e-5 + 1e-5, "dw over 4 GB")
+    out = torch.empty(rows, wide, dtype=BF16, device="cuda")
+    L.moe_group_matmul_t(dy, off, w, out)
+    ref = torch.stack([w[g].double().t().contiguous() @ dy[i].double() for g, i in zip(group.tolist(), at.tolist())])
+    _close(out[at], _f64(ref), np.abs(_f64(ref)) * 2.0**-8 + 1e-4, "y past 4 GB")
+
+
+def test_many_groups():
+    """The largest number of groups, most of them empty."""
+    groups, n, k = 1024, 72, 64
+    counts = np.zeros(groups, np.int64)
+    counts[[0, 1, 63, 64, 511, 700, 1023]] = [3, 70, 1, 130, 2, 5, 9]
+    c = Case(counts.tolist(), n, k, BF16, k)
+    whole, y = c.out(n, F32)
+    L.moe_group_matmul(c.x, c.offsets, c.w, y)
+    ref = OG.matmul(c.xg, c.offsets_h, c.wf, c.rows)
+    c.check(whole, y, ref, _sum_tol(c.xg, c.wf, k, c.offsets_h, c.rows, OG.matmul) + _half_step(ref, F32), "1024 groups")
+
+
 # ----------------------------------------------------------------------------- dispatch
 @pytest.mark.parametrize("rows,top_k,groups", [(1, 1, 1), (8, 6, 384), (4, 2, 16), (341, 6, 384), (342, 6, 384), (1024, 2, 1),
                                                (1025, 2, 1024), (3000, 3, 7), (2731, 3, 128), (20000, 8, 1024), (0, 3, 5)])
