@@ -460,9 +460,9 @@ def _addresses(fn, stream, *tensors):
     for t in tensors:
         if t is None:
             out.append(None)
-        elif t.get_device() != dev:
-            raise MoeError(fn, MOE_EINVAL)
         else:
+            if t.get_device() != dev:
+                raise MoeError(fn, MOE_EINVAL)
             out.append(t.data_ptr())
     return out
 
@@ -478,7 +478,7 @@ def _rows(fn, t):
 
 
 def _ints(fn, t, n):
-    if _type_of(t) != -1:
+    if _types.get(t.dtype) != -1 and _type_of(t) != -1:
         raise MoeError(fn, MOE_EFORMAT)
     if t.numel() != n or not t.is_contiguous():
         raise MoeError(fn, MOE_ESHAPE)
@@ -503,9 +503,11 @@ def moe_group_plan(idx, n_groups, offsets, pairs, pos, ws=None, stream=None):
                                     0 if ws is None else ws.numel() * ws.element_size(), st))
 
 
-def _group_dims(fn, x, src, src_div, offsets, rows, w, out_type):
+def _group_dims(fn, x, src, src_div, offsets, rows, w, out):
     """(GroupDims with everything but ldy and ld_pre, columns of x), x the operand that src selects rows of."""
-    kind = _type(fn, x)
+    kind, out_type = _types.get(x.dtype, -2), _types.get(out.dtype, -2)
+    if kind < 0 or out_type < 0:
+        kind, out_type = _type(fn, x), _type(fn, out)
     if w.dim() != 3:
         raise MoeError(fn, MOE_ESHAPE)
     (groups, n, k), (stride, ldw, one) = w.shape, w.stride()
@@ -523,21 +525,21 @@ def _product(fn, call, x, offsets, w, y, src, src_div, back, stream, pre=None, f
     """factor: None without pre, else the columns of (y, pre) per column of the product, times two."""
     s, xa, oa, wa, ya, sa, pa = _addresses(fn, stream, x, offsets, w, y, src, pre)
     rows, y_cols, ldy = _rows(fn, y)
-    d, x_cols = _group_dims(fn, x, src, src_div, offsets, rows, w, _type(fn, y))
+    d, x_cols = _group_dims(fn, x, src, src_div, offsets, rows, w, y)
     d.ldy = ldy
     x_want, cols = (d.n, d.k) if back else (d.k, d.n)
     if x.dtype != w.dtype or x_cols != x_want or 2 * y_cols != cols * (factor[0] if factor else 2):
         raise MoeError(fn, MOE_ESHAPE)
-    d_ref = ctypes.byref(d)
     if factor is None:
-        st = call(d_ref, xa, sa, oa, wa, ya, s)
+        st = call(d, xa, sa, oa, wa, ya, s)
     else:
         if pre is not None:
             p_rows, p_cols, d.ld_pre = _rows(fn, pre)
             if pre.dtype != x.dtype or p_rows != rows or 2 * p_cols != cols * factor[1]:
                 raise MoeError(fn, MOE_ESHAPE)
-        st = call(d_ref, xa, sa, oa, wa, pa, ya, s) if back else call(d_ref, xa, sa, oa, wa, ya, pa, s)
-    _check(fn, st)
+        st = call(d, xa, sa, oa, wa, pa, ya, s) if back else call(d, xa, sa, oa, wa, ya, pa, s)
+    if st:
+        raise MoeError(fn, st)
 
 
 def moe_group_matmul(x, offsets, w, y, src=None, src_div=1, stream=None):
@@ -569,11 +571,11 @@ def moe_group_wgrad(dy, x, offsets, dw, src=None, src_div=1, accumulate=False, s
     fn = "moe_group_wgrad"
     s, dya, xa, oa, dwa, sa = _addresses(fn, stream, dy, x, offsets, dw, src)
     rows, n, ldy = _rows(fn, dy)
-    d, x_cols = _group_dims(fn, x, src, src_div, offsets, rows, dw, _type(fn, dw))
+    d, x_cols = _group_dims(fn, x, src, src_div, offsets, rows, dw, dw)
     d.ldy = ldy
     if dy.dtype != x.dtype or x_cols != d.k or n != d.n:
         raise MoeError(fn, MOE_ESHAPE)
-    _check(fn, lib().moe_group_wgrad(ctypes.byref(d), dya, xa, sa, oa, dwa, 1 if accumulate else 0, s))
+    _check(fn, lib().moe_group_wgrad(d, dya, xa, sa, oa, dwa, 1 if accumulate else 0, s))
 
 
 def _combine_dims(fn, o_rows, ldo, y, pos, wts, top_k, in_type, out_type):
@@ -599,7 +601,7 @@ def moe_group_combine(o, pos, wts, y, top_k=None, stream=None):
     o_rows, n, ldo = _rows(fn, o)
     d = _combine_dims(fn, o_rows, ldo, y, pos, wts, _top_k(fn, y.shape[0], pos, wts, o_rows, top_k), kind, out)
     _need(fn, d.n == n)
-    _check(fn, lib().moe_group_combine(ctypes.byref(d), oa, pa, wa, ya, s))
+    _check(fn, lib().moe_group_combine(d, oa, pa, wa, ya, s))
 
 
 def moe_group_combine_grad(dy, o, pos, wts, d_o, d_wts, top_k=None, stream=None):
@@ -618,7 +620,7 @@ def moe_group_combine_grad(dy, o, pos, wts, d_o, d_wts, top_k=None, stream=None)
     _need(fn, d.n == n)
     if d_wts is not None:
         _need(fn, _type(fn, d_wts) == T_F32 and d_wts.is_contiguous() and d_wts.shape == (d.rows, top_k))
-    _check(fn, lib().moe_group_combine_grad(ctypes.byref(d), dya, oa, pa, wa, doa, dwa, s))
+    _check(fn, lib().moe_group_combine_grad(d, dya, oa, pa, wa, doa, dwa, s))
 
 
 # ----------------------------------------------------------------------------- 4-bit matrix-vector products
@@ -670,7 +672,7 @@ def moe_q4_matvec(x, codes, scales, zeros, group, y, idx=None, x_div=1, swiglu=F
         if t is not None and (t.numel() * t.element_size() < need * n_mats or not t.is_contiguous()):
             raise MoeError(fn, MOE_ESHAPE)
     d = Q4Dims(n, k, group, n_mats, rows, x_div, kind, out, 1 if swiglu else 0, ldx, ldy)
-    _check(fn, lib().moe_q4_matvec(ctypes.byref(d), xa, ia, ca, sa, za, ya, s))
+    _check(fn, lib().moe_q4_matvec(d, xa, ia, ca, sa, za, ya, s))
 
 
 @functools.lru_cache(maxsize=256)
