@@ -713,7 +713,9 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
   }
   if constexpr (!QA) {
     const bool gather = a.src != nullptr;
-    fq.buf = gather ? buffer_of(a.q, a.src_rows, a.ldq, a.nr) : buffer_of(a.q + it.q0 * a.ldq, it.end - it.q0, a.ldq, a.nr);
+    // of a group, only the tile's rows: all of them may pass 4 GiB
+    fq.buf = gather ? buffer_of(a.q, a.src_rows, a.ldq, a.nr)
+                    : buffer_of(a.q + it.q0 * a.ldq, it.end - it.q0 < BQ ? it.end - it.q0 : BQ, a.ldq, a.nr);
     fq.step = kRed * 2;
 #pragma unroll
     for (int i = 0; i < fq.N; ++i) {

@@ -337,6 +337,23 @@ def test_operands_past_32_bit_offsets():
     _close(out[at], _f64(ref), np.abs(_f64(ref)) * 2.0**-8 + 1e-4, "y past 4 GB")
 
 
+def test_group_of_just_over_4_gib():
+    """One group's rows, ungathered, of 2^32 bytes and ten rows more: its first tile holds whole rows all the same."""
+    rows, wide, narrow = (1 << 19) + 10, 4096, 64
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.zeros(rows, wide, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 9, 10, 100, 255, 256, 300, 524_287, rows - 1], device="cuda")
+    x[at] = torch.randn(len(at), wide, generator=gen, device="cuda").to(BF16)
+    w = (torch.randn(1, narrow, wide, generator=gen, device="cuda") * 0.05).to(BF16)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    for n in (narrow, 1):                        # 1: columns of another tile shape
+        y = torch.empty(rows, n, device="cuda")
+        L.moe_group_matmul(x, off, w[:, :n], y)
+        ref = x[at].double() @ w[0, :n].double().t().contiguous()
+        _close(y[at], _f64(ref), np.abs(_f64(ref)) * 1e-5 + wide * 2.0**-24 * 4, f"{n} columns")
+        assert int((y != 0).any(1).sum()) == len(at)
+
+
 def test_many_groups():
     """The largest number of groups, most of them empty."""
     groups, n, k = 1024, 72, 64
