@@ -1056,7 +1056,7 @@ Gemm products(const moe_group_dims* d, const void* x, const int32_t* src, const 
   a.ldq = d->ldx;
   a.p_stride = d->w_stride;
   a.np = np;
-  a.nr = nr;
+  a.nr = d->x_rows ? nr : 0;   // no row to read: every sum is empty
   return a;
 }
 
@@ -1072,7 +1072,7 @@ int moe_group_matmul(const moe_group_dims* d, const void* x, const int32_t* src,
                      const void* w, void* y, void* stream) {
   if (int st = check_group(d, kMatmul, src, false)) return st;
   if (d->rows == 0) return MOE_OK;
-  if (!x || !offsets || !w || !y) return MOE_EINVAL;
+  if ((!x && d->x_rows) || !offsets || !w || !y) return MOE_EINVAL;
   return launch_type<false, false, kStore>(d, products(d, x, src, offsets, w, y, d->n, d->k), stream);
 }
 
@@ -1080,7 +1080,7 @@ int moe_group_swiglu(const moe_group_dims* d, const void* x, const int32_t* src,
                      const void* w, void* h, void* pre, void* stream) {
   if (int st = check_group(d, kSwiglu, src, pre)) return st;
   if (d->rows == 0) return MOE_OK;
-  if (!x || !offsets || !w || !h) return MOE_EINVAL;
+  if ((!x && d->x_rows) || !offsets || !w || !h) return MOE_EINVAL;
   Gemm a = products(d, x, src, offsets, w, h, d->n, d->k);
   a.half = d->n / 2;
   a.pre_out = static_cast<uint16_t*>(pre);
@@ -1091,7 +1091,7 @@ int moe_group_matmul_t(const moe_group_dims* d, const void* dy, const int32_t* s
                        const void* w, void* dx, void* stream) {
   if (int st = check_group(d, kMatmulT, src, false)) return st;
   if (d->rows == 0) return MOE_OK;
-  if (!dy || !offsets || !w || !dx) return MOE_EINVAL;
+  if ((!dy && d->x_rows) || !offsets || !w || !dx) return MOE_EINVAL;
   return launch_type<true, false, kStore>(d, products(d, dy, src, offsets, w, dx, d->k, d->n), stream);
 }
 
@@ -1099,9 +1099,8 @@ int moe_group_swiglu_grad(const moe_group_dims* d, const void* dy, const int32_t
                           const void* w, const void* pre, void* dpre, void* stream) {
   if (int st = check_group(d, kSwigluGrad, src, true)) return st;
   if (d->rows == 0) return MOE_OK;
-  if (!dy || !offsets || !w || !pre || !dpre) return MOE_EINVAL;
+  if ((!dy && d->x_rows) || !offsets || !w || !pre || !dpre) return MOE_EINVAL;
   Gemm a = products(d, dy, src, offsets, w, dpre, d->k, d->n);
-  a.half = d->k;
   a.pre_in = static_cast<const uint16_t*>(pre);
   return launch_type<true, false, kSwigluBack>(d, a, stream);
 }
@@ -1109,8 +1108,9 @@ int moe_group_swiglu_grad(const moe_group_dims* d, const void* dy, const int32_t
 int moe_group_wgrad(const moe_group_dims* d, const void* dy, const void* x, const int32_t* src,
                     const int32_t* offsets, void* dw, int32_t accumulate, void* stream) {
   if (int st = check_group(d, kWgrad, src, false)) return st;
-  if (!offsets || !dw || (d->rows && (!dy || !x))) return MOE_EINVAL;
+  if (!offsets || !dw || (d->rows && (!dy || (!x && d->x_rows)))) return MOE_EINVAL;
   Gemm a = common(d, src, offsets);
+  if (d->x_rows == 0) a.rows = 0;   // no row to read: every group is empty
   a.p = static_cast<const uint16_t*>(x);
   a.q = static_cast<const uint16_t*>(dy);
   a.y = dw;

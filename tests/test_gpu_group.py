@@ -208,6 +208,23 @@ def test_weight_gradient_without_rows_is_zero():
     assert bool((dw == 0).all())
 
 
+@pytest.mark.parametrize("n,k", [(64, 128), (33, 51)])
+def test_operand_without_rows(n, k):
+    """src given and no row that it could name: products and gradients of zeros."""
+    off = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
+    src = torch.tensor([-1, 0, 3, -1, 1], dtype=torch.int32, device="cuda")
+    x, dy = (torch.empty((0, c), dtype=BF16, device="cuda") for c in (k, n))
+    w = torch.ones((2, n, k), dtype=BF16, device="cuda")
+    full = lambda *s: torch.full(s, SENTINEL, device="cuda")  # noqa: E731
+    y, dx, dw, dpre = full(5, n), full(5, k), full(2, n, k), full(5, 2 * k)
+    L.moe_group_matmul(x, off, w, y, src=src)
+    L.moe_group_matmul_t(dy, off, w, dx, src=src)
+    L.moe_group_swiglu_grad(dy, off, w, torch.ones((5, 2 * k), dtype=BF16, device="cuda"), dpre, src=src)
+    L.moe_group_wgrad(torch.ones((5, n), dtype=BF16, device="cuda"), x, off, dw, src=src)
+    for t in (y, dx, dpre, dw):
+        assert bool((t == 0).all())
+
+
 def test_values_that_are_not_finite_stay_in_their_rows():
     """A NaN or an infinity in one row of x, or past the columns of a strided operand, reaches that row alone."""
     c = Case([5, 9], 70, 100, BF16, 100, pad=4)
