@@ -199,8 +199,7 @@ __device__ __forceinline__ Item find_rows(const Gemm& a) {
   Item it{};
   const int at = xcd_item(total * a.tiles_p);
   const int tile = at / a.tiles_p;
-  it.any = tile < total;
-  if (!it.any) return it;
+  if (tile >= total) return it;
 #pragma unroll
   for (int c = 0; c < kMost; ++c) {
     if (c >= parts) break;
@@ -218,6 +217,9 @@ __device__ __forceinline__ Item find_rows(const Gemm& a) {
     const int wide = tq - 8 * band < 8 ? tq - 8 * band : 8;
     it.p0 = rest / wide * BP;
     it.q0 = it.begin + (8 * band + rest % wide) * BQ;
+    // offsets that do not ascend can make more items than the grid was made
+    // for, past 32 bits too: whatever such a count gives writes nothing
+    it.any = at >= 0 && in >= 0 && it.q0 >= it.begin && it.q0 < it.end;
     break;
   }
   return it;

@@ -258,6 +258,18 @@ def test_offsets_out_of_range_are_clamped():
         assert bool((y[torch.from_numpy(~m).cuda()] == SENTINEL).all())
 
 
+def test_offsets_that_do_not_ascend_write_inside():
+    """Groups that overlap make more tiles than the grid holds: what is written stays inside y."""
+    rows, groups = 200, 64
+    off = torch.tensor([0, rows] * (groups // 2) + [0], dtype=torch.int32, device="cuda")
+    x = torch.ones((rows, 64), dtype=BF16, device="cuda")
+    w = torch.ones((groups, 40, 64), dtype=BF16, device="cuda")
+    whole = torch.full((3 * rows, 40), SENTINEL, device="cuda")
+    L.moe_group_matmul(x, off, w, whole[rows:2 * rows])
+    assert bool((whole[:rows] == SENTINEL).all()) and bool((whole[2 * rows:] == SENTINEL).all())
+    assert bool(((whole[rows:2 * rows] == 64) | (whole[rows:2 * rows] == SENTINEL)).all())
+
+
 # ----------------------------------------------------------------------------- large
 def _device_reference(way, x, w, bounds, src=None, div=1):
     """fp64 on the GPU: the same definitions for sizes that take the large tiles."""
