@@ -641,6 +641,9 @@ typedef struct {
  *          idx of moe_route), or NULL: matrix 0 for every row.  -1: the row of
  *          y is 0 (a pair computed elsewhere); any other id outside
  *          [0, n_mats): NaN.  Rows of one matrix read it once per call.
+ *   x      |x| < 2^114 (a group's sum is taken as the difference of two that are
+ *          up to 31 * 128 times as large); a row that holds an infinity or a
+ *          NaN comes out NaN
  *   codes, scales, zeros (or NULL): 16-byte aligned */
 int moe_q4_matvec(const moe_q4_dims* d, const void* x, const int32_t* idx, const void* codes, const void* scales,
                   const void* zeros, void* y, void* stream);

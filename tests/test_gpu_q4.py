@@ -116,6 +116,21 @@ def test_values_that_are_not_finite_stay_in_their_rows():
     assert not fine[4] and not fine[17] and fine.sum() == 18
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+def test_large_and_infinite_values(zeros):
+    """Values just below the documented bound are exact to the usual tolerance, a row with an infinity is NaN."""
+    n, k, group = 32, 256, 128
+    w = Weights(1, n, k, group, zeros)
+    xs = np.random.default_rng(5).uniform(-1, 1, (3, k))
+    x = (torch.from_numpy(xs) * 2.0**113).to(BF16).cuda()
+    x[1, 200] = float("inf")
+    y = torch.empty((3, n), device="cuda")
+    L.moe_q4_matvec(x, w.codes, w.scales, w.zeros, group, y)
+    ref, tol = w.product(_f64(x[::2]) * 2.0**-113, [0, 0], False, F32)
+    _close(y[::2] * 2.0**-113, ref, tol)
+    assert bool(torch.isnan(y[1]).all())
+
+
 def test_layer_of_4_bit_experts_for_one_step():
     """Route's idx and weights -> gate/up + SwiGLU -> down -> combine, captured and replayed."""
     rows, top_k, mats, hidden, inter, group = 3, 2, 5, 160, 96, 32
