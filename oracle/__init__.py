@@ -18,6 +18,8 @@ Modules:
   formats  -- byte layouts, RTN packers (fp32 arithmetic) and exact fp64 decoders
   moe      -- router, top-k selection, softmax renormalisation, SwiGLU experts,
               weighted combine, MXFP8 activation quantiser
+  group    -- dispatch, grouped products, SwiGLU, combine and their gradients at
+              any shape, the 4-bit group format
   sizes    -- the pages' byte arithmetic (params per expert, bytes per token,
               mixed-format averages, bandwidth ceilings)
 
