@@ -363,6 +363,72 @@ struct Rows {
   }
 };
 
+// The SwiGLU gradient's epilogue.  dh goes through LDS, 16 rows at a time; a lane
+// then holds eight columns of a row.  Their gate and up are asked for two such
+// pieces ahead, and without a branch when the tile is whole: the compiler then
+// waits for those loads alone, not for the stores behind them.
+template <bool BF, int TP, int TQ, bool WHOLE>
+__device__ __forceinline__ void swiglu_back(const Gemm& a, f32x4 (&acc)[TP / 16][TQ / 16], int c0, int q_first, int q_end,
+                                            void* y, const Rows<TP>& rows) {
+  constexpr int kPieces = TP / 32, kAhead = TQ / 16 < 2 ? 1 : 2;
+  static_assert(TP % 32 == 0, "whole pieces of 16 rows by 32 columns");
+  const int l = threadIdx.x & 63;
+  uint8_t* y2 = static_cast<uint8_t*>(y) + static_cast<int64_t>(a.np) * (a.out_type == MOE_T_F32 ? 4 : 2);
+  u32x4 gate[kAhead][kPieces], up[kAhead][kPieces];
+  const auto ask = [&](int j) {
+#pragma unroll
+    for (int s = 0; s < kPieces; ++s) {
+      const int r = q_first + j * 16 + (s * 64 + l) / (TP / 8), c = c0 + (s * 64 + l) % (TP / 8) * 8;
+      u32x4 &g = gate[j % kAhead][s], &u = up[j % kAhead][s];
+      if constexpr (!WHOLE) {
+        g = u = u32x4{0, 0, 0, 0};
+        if (r >= q_end || c >= a.np) continue;
+      }
+      const uint16_t* at = a.pre_in + r * a.ld_pre + c;
+      if (WHOLE || c + 8 <= a.np) {
+        __builtin_memcpy(&g, at, 16);
+        __builtin_memcpy(&u, at + a.np, 16);
+      } else {
+        for (int e = 0; e < 8; ++e)
+          if (c + e < a.np) {
+            g[e / 2] |= static_cast<uint32_t>(at[e]) << 16 * (e & 1);
+            u[e / 2] |= static_cast<uint32_t>(at[a.np + e]) << 16 * (e & 1);
+          }
+      }
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) ask(j);
+#pragma unroll
+  for (int j = 0; j < TQ / 16; ++j) {
+    if (!WHOLE && q_first + j * 16 >= q_end) break;
+#pragma unroll
+    for (int i = 0; i < TP / 16; ++i) rows.put(i, acc[i][j]);
+#pragma unroll
+    for (int s = 0; s < kPieces; ++s) {
+      const int rl = (s * 64 + l) / (TP / 8), cl = (s * 64 + l) % (TP / 8) * 8, r = q_first + j * 16 + rl, c = c0 + cl;
+      if (!WHOLE && (r >= q_end || c >= a.np)) continue;
+      const MOE_LDS uint8_t* at = rows.at + rl * rows.kPitch + cl * 4;
+      f32x4 dh[2], dg[2], du[2];
+      dh[0] = *reinterpret_cast<const MOE_LDS f32x4*>(at);
+      dh[1] = *reinterpret_cast<const MOE_LDS f32x4*>(at + 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = from_half<BF>(static_cast<uint16_t>(gate[j % kAhead][s][e / 2] >> 16 * (e & 1)));
+        const float u = from_half<BF>(static_cast<uint16_t>(up[j % kAhead][s][e / 2] >> 16 * (e & 1)));
+        const float sg = 1.0f / (1.0f + __expf(-g)), d = dh[e / 4][e % 4];
+        dg[e / 4][e % 4] = d * u * sg * (1.0f + g * (1.0f - sg));
+        du[e / 4][e % 4] = d * g * sg;
+      }
+      const int64_t o = r * a.ldy + c;
+      const int n = WHOLE ? 8 : a.np - c;
+      store8(y, o, dg, n, a.out_type);
+      store8(y2, o, du, n, a.out_type);
+    }
+    if (j + kAhead < TQ / 16) ask(j + kAhead);
+  }
+}
+
 // `lds`: room for a Rows<TP> a wave; every wave's tile reads are done.
 template <bool BF, int EPI, int TP, int TQ>
 __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&acc)[TP / 16][TQ / 16], int wp, int wq,
@@ -371,6 +437,12 @@ __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&
   const int type = BF ? MOE_T_BF16 : MOE_T_F16;
   const Rows<C> rows{lds + wave_id() * Rows<C>::kBytes};
   const int c0 = (EPI == kSwigluOut ? it.p0 / 2 : it.p0) + wp * C;
+  if constexpr (EPI == kSwigluBack) {
+    const int q0 = it.q0 + wq * TQ;
+    if (q0 + TQ <= q_end && c0 + TP <= a.np) swiglu_back<BF, TP, TQ, true>(a, acc, c0, q0, q_end, y, rows);
+    else if (q0 < q_end) swiglu_back<BF, TP, TQ, false>(a, acc, c0, q0, q_end, y, rows);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < TQ / 16; ++j) {
     const int q0 = it.q0 + wq * TQ + j * 16;
@@ -397,52 +469,6 @@ __device__ __forceinline__ void epilogue(const Gemm& a, const Item& it, f32x4 (&
 #pragma unroll
         for (int i = 0; i < TP / 32; ++i) rows.put(i, acc[i + TP / 32][j]);
         rows.flush(a.pre_out + a.half, a.ld_pre, q0, q_end, c0, a.half, type, false);
-      }
-    } else {
-      // dh goes through LDS; a lane then holds eight columns of a row, whose
-      // gate and up it has asked for before
-      constexpr int kPieces = (C + 31) / 32;
-      const int l = threadIdx.x & 63;
-      u32x4 gate[kPieces], up[kPieces];
-#pragma unroll
-      for (int s = 0; s < kPieces; ++s) {
-        const int r = (s * 64 + l) / (C / 8), c = c0 + (s * 64 + l) % (C / 8) * 8;
-        gate[s] = up[s] = u32x4{0, 0, 0, 0};
-        if (r >= 16 || q0 + r >= q_end || c >= a.np) continue;
-        const uint16_t* at = a.pre_in + static_cast<int64_t>(q0 + r) * a.ld_pre + c;
-        if (c + 8 <= a.np) {
-          __builtin_memcpy(&gate[s], at, 16);
-          __builtin_memcpy(&up[s], at + a.np, 16);
-        } else {
-          for (int e = 0; e < 8; ++e)
-            if (c + e < a.np) {
-              gate[s][e / 2] |= static_cast<uint32_t>(at[e]) << 16 * (e & 1);
-              up[s][e / 2] |= static_cast<uint32_t>(at[a.np + e]) << 16 * (e & 1);
-            }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < TP / 16; ++i) rows.put(i, acc[i][j]);
-      uint8_t* y2 = static_cast<uint8_t*>(y) + static_cast<int64_t>(a.np) * (a.out_type == MOE_T_F32 ? 4 : 2);
-#pragma unroll
-      for (int s = 0; s < kPieces; ++s) {
-        const int r = (s * 64 + l) / (C / 8), cl = (s * 64 + l) % (C / 8) * 8, c = c0 + cl;
-        if (r >= 16 || q0 + r >= q_end || c >= a.np) continue;
-        const MOE_LDS uint8_t* at = rows.at + r * rows.kPitch + cl * 4;
-        f32x4 dh[2], dg[2], du[2];
-        dh[0] = *reinterpret_cast<const MOE_LDS f32x4*>(at);
-        dh[1] = *reinterpret_cast<const MOE_LDS f32x4*>(at + 16);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float g = from_half<BF>(static_cast<uint16_t>(gate[s][e / 2] >> 16 * (e & 1)));
-          const float u = from_half<BF>(static_cast<uint16_t>(up[s][e / 2] >> 16 * (e & 1)));
-          const float sg = 1.0f / (1.0f + __expf(-g)), d = dh[e / 4][e % 4];
-          dg[e / 4][e % 4] = d * u * sg * (1.0f + g * (1.0f - sg));
-          du[e / 4][e % 4] = d * g * sg;
-        }
-        const int64_t o = (q0 + r) * a.ldy + c;
-        store8(y, o, dg, a.np - c, a.out_type);
-        store8(y2, o, du, a.np - c, a.out_type);
       }
     }
   }
