@@ -15,11 +15,12 @@
 //
 // Bound by the matrix cores with many rows a group, by the weights' bytes with
 // few.  Measured, bf16:
-//     8192^3, one group: y 848 us (1297 TFLOP/s), SwiGLU 752, dx 767 (1433), fp32
-//       dW 821 (1339); the same operations in a library's product: 772
-//     16 groups of 1024 rows, n 4608, k 5120: y 716 us (1079), dx 676 (1144), fp32
-//       dW 828 (934, 1.5 GB written)
-//     384 groups of 32 rows, the same matrices: y 3159 us, 5.8 TB/s; dx 3278
+//     8192^3, one group: y 898 us (1224 TFLOP/s), SwiGLU 806, dx 827 (1330), fp32
+//       dW 844 (1302); the same operations in a library's product: 772 (another
+//       card of the same model ran all of ours 5 % faster)
+//     16 groups of 1024 rows, n 4608, k 5120: y 681 us (1135), dx 691 (1119), fp32
+//       dW 864 (895, 1.5 GB written)
+//     384 groups of 32 rows, the same matrices: y 3150 us, 5.8 TB/s; dx 3274
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -716,9 +717,11 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
   constexpr int TP = BP / WP, TQ = BQ / WQ, NW = WP * WQ;
   constexpr bool kWeight = PA && QA;   // wgrad
   constexpr int kStep = (BP + BQ) * 128, kStage = SPLIT * kStep;
+  constexpr bool kPhased = STAGES == 2 && NW == 8 && SPLIT == 1;   // two groups of waves, a phase apart
+  constexpr int kLds = STAGES * kStage + (kPhased ? BP * 128 : 0);
   static_assert(SPLIT == 1 || (SPLIT - 1) * BP * BQ * 4 <= STAGES * kStage, "the groups' sums use the tiles' memory");
   static_assert(NW * Rows<TP>::kBytes + (SPLIT - 1) * BP * BQ * 4 <= STAGES * kStage, "the epilogue's rows use the tiles' memory");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const Item it = kWeight ? find_matrix<BP, BQ>(a) : find_rows<BP, BQ>(a);
   if (!it.any) return;
   const int wave = wave_id() % NW, turn = wave_id() / NW, wp = wave % WP, wq = wave / WP;
@@ -770,7 +773,7 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
 
   // wgrad: the rows of x follow src.  A load covers kR of them, the same for
   // the whole wave, so their entries come through scalar loads (which no
-  // vector-memory count waits for), a step before they are used.
+  // vector-memory count waits for), a phase or more before they are used.
   constexpr int kR = PA ? Feed<PA, BP, NW>::kRowsPerLoad : 1, kNext = decltype(fp)::N * kR;
   [[maybe_unused]] int32_t next[kNext];
   const auto fetch = [&](int m) {
@@ -791,9 +794,8 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
   fetch(0);
 
   // stage m holds steps m * SPLIT .. ; this group's is `turn` of them
-  const auto issue = [&](int m) {
+  const auto issue_p = [&](int m, MOE_LDS uint8_t* tp) {
     const int t = m * SPLIT + turn;
-    MOE_LDS uint8_t* tp = base + m % STAGES * kStage;
     if (kWeight && a.src) {
       const int sub = (threadIdx.x & 63) / (BP / 8);   // which of a load's rows
 #pragma unroll
@@ -810,14 +812,16 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
     } else {
       fp.load(tp, t);
     }
-    fq.load(tp + BP * 128, t);
+  };
+  const auto issue = [&](int m) {
+    MOE_LDS uint8_t* tp = base + m % STAGES * kStage;
+    issue_p(m, tp);
+    fq.load(tp + BP * 128, m * SPLIT + turn);
   };
 
   f32x4 acc[TP / 16][TQ / 16] = {};
   s16x8 vp[TP / 16], vq[TQ / 16];
-  const auto read = [&](int t, int kk) {
-    const MOE_LDS uint8_t* lp = base + t % STAGES * kStage;
-    const MOE_LDS uint8_t* lq = lp + BP * 128;
+  const auto read = [&](const MOE_LDS uint8_t* lp, const MOE_LDS uint8_t* lq, int kk) {
 #pragma unroll
     for (int i = 0; i < TP / 16; ++i) vp[i] = fragment<PA, BP>(lp, wp * TP + i * 16, kk);
 #pragma unroll
@@ -830,39 +834,55 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
       for (int j = 0; j < TQ / 16; ++j) acc[i][j] = mma<BF>(vp[i], vq[j], acc[i][j]);
   };
   const int steps = (red + kRed * SPLIT - 1) / (kRed * SPLIT);
-  if constexpr (STAGES == 2 && NW == 8 && SPLIT == 1) {
+  if constexpr (kPhased) {
     // Two waves share a SIMD, and four of the eight run one phase behind the
     // other four: while one wave of a SIMD multiplies, the other one reads its
     // next fragments and issues loads, so the matrix cores see no gap.  A step
     // is four phases (read and multiply each half of the 64), with a barrier
-    // after each.  The tile of step t + 1 is loaded over that of step t - 1,
-    // whose last reader was done a phase before step t began, and has landed
-    // at the end of the fourth phase of step t: the leading waves wait there,
-    // the others in their third phase, which ends at the same barrier.  8192^3
-    // went from 1141 to 1230 TFLOP/s with it, its input gradient from 1017 to
-    // 1291, its weight gradient from 972 to 1268.  Five stages of half the
-    // length were 8 - 15 % slower than these two.
+    // after each.  Step t loads Q of step t + 1 and then P of step t + 2, both
+    // over tiles of step t - 1, whose last reader was done a phase before step t
+    // began.  Q and P of step t + 1 have landed at the end of the fourth phase
+    // of step t, when only the last loads, of P, may be in flight: the leading
+    // waves wait there, the others in their third phase, which ends at the same
+    // barrier.  8192^3 went from 1141 to 1230 TFLOP/s with the phases, its input
+    // gradient from 1017 to 1291, its weight gradient from 972 to 1268.  Five
+    // stages of half the length for both operands were 8 - 15 % slower than two.
+    // P (the weights, in the products) a step earlier takes the LDS that is
+    // left: 16 groups of 1024 rows, n 4608, k 5120 724 -> 681 us, 128 of 192
+    // 1539 -> 1448, its weight gradient 2308 -> 2189; 8192^3, whose operands the
+    // last cache holds, 885 -> 898.
     const bool behind = wave >= 4;
-    issue(0);
+    constexpr int kTileP = BP * 128, kTileQ = BQ * 128, kLate = decltype(fp)::N;
+    MOE_LDS uint8_t *p0 = base, *p1 = base + kTileP, *p2 = base + 2 * kTileP;   // of P: this step's, the next two
+    MOE_LDS uint8_t* const lq = base + 3 * kTileP;
+    fq.load(lq, 0);
+    issue_p(0, p0);
     fetch(1);
-    step_barrier<0>();
+    issue_p(1, p1);
+    fetch(2);
+    step_barrier<kLate>();
     if (behind) asm volatile("s_barrier" ::: "memory");
     for (int t = 0; t < steps; ++t) {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        read(t, kk);
-        if (kk == 0) issue(t + 1);
-        if (kk == 1 && behind) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        read(p0, lq + (t & 1) * kTileQ, kk);
+        if (kk == 0) {
+          fq.load(lq + (~t & 1) * kTileQ, t + 1);
+          issue_p(t + 2, p2);
+        }
+        if (kk == 1 && behind) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLate) : "memory");
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (kk == 0) fetch(t + 2);   // waited for with the next fragments, a phase from here
+        if (kk == 0) fetch(t + 3);   // waited for with the next fragments, a phase from here
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
         multiply();
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
-        if (kk == 1 && !behind) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (kk == 1 && !behind) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLate) : "memory");
         asm volatile("s_barrier" ::: "memory");
       }
+      MOE_LDS uint8_t* done = p0;
+      p0 = p1, p1 = p2, p2 = done;
     }
     if (!behind) asm volatile("s_barrier" ::: "memory");
   } else {
@@ -879,7 +899,7 @@ __global__ __launch_bounds__(64 * WP * WQ * SPLIT) void k_group_tiles(Gemm a) {
       fetch(t + STAGES);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        read(t, kk);
+        read(base + t % STAGES * kStage, base + t % STAGES * kStage + BP * 128, kk);
         multiply();
       }
     }
